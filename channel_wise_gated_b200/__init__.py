@@ -8,6 +8,11 @@ check their dtypes, shapes and contiguity, and pass raw pointers through.
     o, hT = chunk_fwd(q, k, v, log_alpha, beta, h0=None, cu_seqlens=None)
     o     = decode_step(q, k, v, log_alpha, beta, state)      # state updated in place
     o     = decode_tokens(q, k, v, log_alpha, beta, state)    # t tokens per sequence
+    o     = decode_tree(q, k, v, log_alpha, beta, state, tree)  # a tree of drafted tokens
+
+The latent-attention (MLA) layers that alternate with KDA layers, over a paged cache:
+
+    mla_append(x, norm_w, cache, page_table, cache_lens, cu_seqlens)
 """
 
 from __future__ import annotations
@@ -20,6 +25,9 @@ from . import _native
 from ._native import KdaError  # noqa: F401
 
 D = 128
+MLA_LATENT = 512                        # latent values per token, shared by all heads
+MLA_SHARED = 64                         # key values per token that the heads share as they are
+MLA_WIDTH = MLA_LATENT + MLA_SHARED     # values cached per token
 
 # Arithmetic type of the prefill contractions for bf16 inputs (bf16 operands, fp32 accumulation).
 PREFILL_COMPUTE_DTYPE = "bf16"
@@ -321,6 +329,113 @@ def decode_tokens(q, k, v, log_alpha, beta, state, o=None):
                                _stream_ptr(dev))
     _native.check(st, "kda_decode_tokens")
     return o
+
+
+def decode_tree(q, k, v, log_alpha, beta, state, tree=None, o=None):
+    """Outputs of a tree of drafted tokens per (sequence, head); the state is only read.
+
+    q, k, v: [N, t, H, 128] bf16 or fp32, t = 1..16; log_alpha: [N, t, H, 128] and beta:
+    [N, t, H] (bf16 or fp32, same dtype); state: [N, H, 128, 128] fp32; tree: [N, t] int32,
+    bit i of tree[n, r] set if token i is an ancestor of token r or r itself, parents before
+    their children (None: a chain). Token r's output is the recurrence's after the tokens of
+    its path. Returns o like q. The accepted path is then applied with decode_tokens.
+    """
+    lib = _native.load()
+    if q.dim() != 4 or q.shape[3] != D:
+        raise ValueError("q must be [N, t, H, 128]")
+    N, t, H, _ = q.shape
+    if not 1 <= t <= _native.KDA_DECODE_MAX_TOKENS:
+        raise ValueError(f"t must be in 1..{_native.KDA_DECODE_MAX_TOKENS}")
+    dev = q.device
+    if q.dtype not in _DT or log_alpha.dtype not in _DT:
+        raise TypeError("unsupported dtype")
+    for name, x in (("q", q), ("k", k), ("v", v)):
+        _need(x, name, q.dtype, (N, t, H, D), dev)
+    _need(log_alpha, "log_alpha", log_alpha.dtype, (N, t, H, D), dev)
+    _need(beta, "beta", log_alpha.dtype, (N, t, H), dev)
+    _need(state, "state", torch.float32, (N, H, D, D), dev)
+    if tree is not None:
+        _need(tree, "tree", torch.int32, (N, t), dev)
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _need(o, "o", q.dtype, (N, t, H, D), dev)
+    with torch.cuda.device(dev):
+        st = lib.kda_decode_tree(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta),
+                                 _ptr(state), _ptr(tree), _ptr(o), N, t, H, _DT[q.dtype],
+                                 _DT[log_alpha.dtype], _stream_ptr(dev))
+    _native.check(st, "kda_decode_tree")
+    return o
+
+
+def _need_rows(t, name, dtype, shape, device):
+    """As _need, for tensors whose last dimension alone must be dense: the strides of the others
+    are passed on, in multiples of 8 elements (16 bytes of bf16)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(-1) != 1 or any(s % 8 for n, s in zip(t.shape, t.stride()[:-1]) if n > 1):
+        raise ValueError(f"{name} must have a dense last dimension and strides in multiples of 8")
+
+
+def _row_stride(t, dim, dense):
+    """The stride of dimension dim; of one entry, where torch may report any, the dense one."""
+    return t.stride(dim) if t.shape[dim] > 1 else dense
+
+
+def _paged_cache(cache, page_table, cache_lens, n_seqs, dev):
+    """Check a paged latent cache; returns (n_pages, page_size, max_pages)."""
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 3 or cache.shape[2] != MLA_WIDTH:
+        raise ValueError("cache must be [n_pages, page_size, 576]")
+    _need(cache, "cache", torch.bfloat16, None, dev)
+    _need(page_table, "page_table", torch.int32, None, dev)
+    if page_table.dim() != 2 or page_table.shape[0] != n_seqs:
+        raise ValueError(f"page_table must be [{n_seqs}, max_pages]")
+    _need(cache_lens, "cache_lens", torch.int32, (n_seqs,), dev)
+    return cache.shape[0], cache.shape[1], page_table.shape[1]
+
+
+def mla_append(x, norm_w, cache, page_table, cache_lens, cu_seqlens=None, latent=None,
+               output_latent: bool = False, eps: float = 1e-6):
+    """Normalise new tokens' latents and write them into the paged cache (in place).
+
+    x: [T, 576] bf16, 512 latent values and the 64 shared key values (rows may be strided, as
+    a slice of a wider projection); norm_w: [512] fp32 RMSNorm weight or None (cached as they
+    are); cache: [n_pages, page_size, 576] bf16; page_table: [N, max_pages] int32; cache_lens:
+    [N] int32, lengths with the new tokens: sequence n's T_n new rows are the last ones before
+    cache_lens[n]; cu_seqlens: [N+1] int32 or None (T / N tokens each). Returns the normalised
+    latents [T, 512] bf16 with output_latent (or into latent), else None.
+    """
+    lib = _native.load()
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be [T, 576]")
+    dev, T = x.device, x.shape[0]
+    _need_rows(x, "x", torch.bfloat16, (T, MLA_WIDTH), None)
+    _need(cache_lens, "cache_lens", torch.int32, None, dev)
+    N = cache_lens.numel()
+    n_pages, page_size, max_pages = _paged_cache(cache, page_table, cache_lens, N, dev)
+    if norm_w is not None:
+        _need(norm_w, "norm_w", torch.float32, (MLA_LATENT,), dev)
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
+    if latent is not None:
+        _need(latent, "latent", torch.bfloat16, (T, MLA_LATENT), dev)
+    elif output_latent:
+        latent = torch.empty((T, MLA_LATENT), dtype=torch.bfloat16, device=dev)
+    with torch.cuda.device(dev):
+        st = lib.kda_mla_append(_ptr(x), _row_stride(x, 0, MLA_WIDTH), _ptr(norm_w), float(eps),
+                                _ptr(cache), n_pages, page_size, _ptr(page_table), max_pages,
+                                _ptr(cache_lens), _ptr(cu_seqlens), N, T, _ptr(latent),
+                                _stream_ptr(dev))
+    _native.check(st, "kda_mla_append")
+    return latent
 
 
 def device_status(device=None) -> int:

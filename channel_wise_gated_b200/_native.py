@@ -25,13 +25,15 @@ KDA_ERR_SEQLENS = -5
 KDA_ERR_CUDA = -6
 KDA_ERR_TIMEOUT = -7
 KDA_ERR_SCRATCH = -8
+KDA_ERR_PAGE = -9
+KDA_ERR_TREE = -10
 
 KDA_DECODE_MAX_TOKENS = 16
 KDA_MAX_SEGMENTS = 64
 SIZE_MAX = ctypes.c_size_t(-1).value
 
 # entry point -> argument types (all return int except kda_status_string)
-_P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+_P, _I32, _I64, _F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 SIGNATURES = {
     "kda_chunk_fwd": [_P, _P, _P, _P, _P, _P, _P, _I32, _I64, _I32, ctypes.c_int, _P, _P, _P],
     "kda_chunk_fwd_simt": [_P, _P, _P, _P, _P, _P, _P, _I32, _I64, _I32, ctypes.c_int, _P, _P, _P],
@@ -51,6 +53,9 @@ SIGNATURES = {
     "kda_decode_step": [_P, _P, _P, _P, _P, _P, _P, _I32, _I32, ctypes.c_int, ctypes.c_int, _P],
     "kda_decode_tokens": [_P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, ctypes.c_int, ctypes.c_int,
                           _P],
+    "kda_decode_tree": [_P, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, ctypes.c_int,
+                        ctypes.c_int, _P],
+    "kda_mla_append": [_P, _I64, _P, _F32, _P, _I64, _I32, _P, _I32, _P, _P, _I32, _I64, _P, _P],
     "kda_testing_chunk_fwd_stall": [_P, _P, _P, _P, _P, _P, _I64, _I32, _P, _P, _I32, ctypes.c_uint32,
                                     _P],
     "kda_device_status": [_P],

@@ -16,7 +16,9 @@
 #include "kda_common.cuh"
 #include "kda_conv.cuh"
 #include "kda_decode.cuh"
+#include "kda_decode_tree.cuh"
 #include "kda_dplr_simt.cuh"
+#include "kda_mla_append.cuh"
 #include "kda_segment.cuh"
 
 // Scratch of kda_chunk_fwd_static, for callers that cannot allocate device memory:
@@ -341,6 +343,31 @@ int launch_decode_tokens(const void* q, const void* k, const void* v, const void
 }
 static_assert(KDA_DECODE_MAX_TOKENS == kda::DEC_MAX_TOKENS, "token limit of the ABI and the kernel");
 
+template <typename TQ, typename TG>
+int launch_decode_tree(const void* q, const void* k, const void* v, const void* log_alpha,
+                       const void* beta, const float* state, const int32_t* tree, void* o,
+                       int32_t n_seqs, int32_t n_tokens, int32_t n_heads, cudaStream_t stream) {
+  const cudaError_t e = kda::launch_decode_tree<TQ, TG>(
+      static_cast<const TQ*>(q), static_cast<const TQ*>(k), static_cast<const TQ*>(v),
+      static_cast<const TG*>(log_alpha), static_cast<const TG*>(beta), state, tree,
+      static_cast<TQ*>(o), n_seqs, n_tokens, n_heads, stream);
+  return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+static_assert(KDA_DECODE_MAX_TOKENS == kda::TREE_MAX_TOKENS, "token limit of the ABI and the kernel");
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The paged latent cache of the mla entry points: sizes and pointers (the table's and the
+// lengths' contents are checked by the kernels).
+int validate_cache(const void* cache, int64_t n_pages, int32_t page_size, const int32_t* page_table,
+                   int32_t max_pages, const int32_t* cache_lens) {
+  if (n_pages <= 0 || n_pages > INT32_MAX || page_size <= 0 || max_pages <= 0) return KDA_ERR_SHAPE;
+  if ((int64_t)max_pages * page_size > (int64_t)INT32_MAX) return KDA_ERR_SHAPE;
+  if (!cache || !page_table || !cache_lens) return KDA_ERR_NULL;
+  if (!aligned16(cache) || !aligned4(page_table) || !aligned4(cache_lens)) return KDA_ERR_ALIGN;
+  return KDA_OK;
+}
+
 // Device address of g_kda_static_scratch in the current context. In host code the
 // array's name only stands in for the symbol, so the address is looked up once per
 // device, with that device current, and kept together with the context it belongs
@@ -652,6 +679,60 @@ int kda_decode_tokens(const void* q, const void* k, const void* v, const void* l
                                             n_heads, stream);
 }
 
+int kda_decode_tree(const void* q, const void* k, const void* v, const void* log_alpha,
+                    const void* beta, const float* state, const int32_t* tree, void* o,
+                    int32_t n_seqs, int32_t n_tokens, int32_t n_heads, kda_dtype qkv_dtype,
+                    kda_dtype gate_dtype, cudaStream_t stream) {
+  if ((qkv_dtype != KDA_F32 && qkv_dtype != KDA_BF16) ||
+      (gate_dtype != KDA_F32 && gate_dtype != KDA_BF16))
+    return KDA_ERR_DTYPE;
+  if (n_seqs <= 0 || n_heads <= 0 || n_tokens <= 0 || n_tokens > KDA_DECODE_MAX_TOKENS ||
+      (int64_t)n_seqs * n_heads > (int64_t)INT32_MAX)
+    return KDA_ERR_SHAPE;
+  if (!q || !k || !v || !log_alpha || !beta || !state || !o) return KDA_ERR_NULL;
+  const void* ptrs[] = {q, k, v, log_alpha, state, o};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return KDA_ERR_ALIGN;
+  if (!aligned4(tree)) return KDA_ERR_ALIGN;
+  using bf = __nv_bfloat16;
+  if (qkv_dtype == KDA_BF16) {
+    if (gate_dtype == KDA_BF16)
+      return launch_decode_tree<bf, bf>(q, k, v, log_alpha, beta, state, tree, o, n_seqs, n_tokens,
+                                        n_heads, stream);
+    return launch_decode_tree<bf, float>(q, k, v, log_alpha, beta, state, tree, o, n_seqs, n_tokens,
+                                         n_heads, stream);
+  }
+  if (gate_dtype == KDA_BF16)
+    return launch_decode_tree<float, bf>(q, k, v, log_alpha, beta, state, tree, o, n_seqs, n_tokens,
+                                         n_heads, stream);
+  return launch_decode_tree<float, float>(q, k, v, log_alpha, beta, state, tree, o, n_seqs, n_tokens,
+                                          n_heads, stream);
+}
+
+int kda_mla_append(const void* x, int64_t x_stride, const float* norm_w, float eps, void* cache,
+                   int64_t n_pages, int32_t page_size, const int32_t* page_table,
+                   int32_t max_pages, const int32_t* cache_lens, const int32_t* cu_seqlens,
+                   int32_t n_seqs, int64_t t_total, void* latent, cudaStream_t stream) {
+  using namespace kda::mla;
+  if (n_seqs <= 0 || t_total < 0 || t_total > INT32_MAX || x_stride < WIDTH || (x_stride & 7) != 0 || !(eps >= 0.f))
+    return KDA_ERR_SHAPE;
+  if (cu_seqlens == nullptr && t_total % n_seqs != 0) return KDA_ERR_SEQLENS;
+  const int st = validate_cache(cache, n_pages, page_size, page_table, max_pages, cache_lens);
+  if (st != KDA_OK) return st;
+  if (t_total == 0) return KDA_OK;
+  if (!x) return KDA_ERR_NULL;
+  if (!aligned16(x) || !aligned16(norm_w) || !aligned16(latent) || !aligned4(cu_seqlens)) return KDA_ERR_ALIGN;
+  const int sms = device_sms();
+  if (sms <= 0) return KDA_ERR_CUDA;
+  constexpr int ROWS = APPEND_THREADS / 32;
+  const int64_t want = (t_total + ROWS - 1) / ROWS, cap = (int64_t)sms * 8;
+  kda_mla_append_kernel<<<(unsigned)(want < cap ? want : cap), APPEND_THREADS, 0, stream>>>(
+      static_cast<const __nv_bfloat16*>(x), x_stride, norm_w, eps, static_cast<__nv_bfloat16*>(cache),
+      n_pages, page_size, page_table, max_pages, cache_lens, cu_seqlens, n_seqs, t_total,
+      static_cast<__nv_bfloat16*>(latent));
+  return launch_status();
+}
+
 int kda_testing_chunk_fwd_stall(const void* q, const void* k, const void* v,
                                 const float* log_alpha, const float* beta, const float* h0,
                                 int64_t t_total, int32_t n_heads, void* o, float* hT,
@@ -680,6 +761,8 @@ int kda_device_status(cudaStream_t stream) {
   }
   if (h & kda::DEVERR_TIMEOUT) return KDA_ERR_TIMEOUT;
   if (h & kda::DEVERR_SEQLENS) return KDA_ERR_SEQLENS;
+  if (h & kda::DEVERR_PAGE) return KDA_ERR_PAGE;
+  if (h & kda::DEVERR_TREE) return KDA_ERR_TREE;
   return KDA_OK;
 }
 
@@ -695,6 +778,8 @@ const char* kda_status_string(int status) {
     case KDA_ERR_TIMEOUT: return "KDA_ERR_TIMEOUT: a kernel gave up a bounded wait";
     case KDA_ERR_SCRATCH:
       return "KDA_ERR_SCRATCH: the call needs more scratch than the library's static array holds";
+    case KDA_ERR_PAGE: return "KDA_ERR_PAGE: a cached position has no page in range";
+    case KDA_ERR_TREE: return "KDA_ERR_TREE: a row of ancestor bits is not a path";
     default: return "unknown kda_status";
   }
 }

@@ -11,7 +11,7 @@ constexpr int D = 128;      // d_k = d_v
 constexpr int CHUNK = 64;   // chunk length of the chunkwise form (appendix C: chunk_size = 64)
 
 // Bits of the device-side error word read back by kda_device_status().
-enum : int { DEVERR_SEQLENS = 1, DEVERR_TIMEOUT = 2 };
+enum : int { DEVERR_SEQLENS = 1, DEVERR_TIMEOUT = 2, DEVERR_PAGE = 4, DEVERR_TREE = 8 };
 
 }  // namespace kda
 

@@ -59,8 +59,12 @@ typedef enum {
   KDA_ERR_SEQLENS = -5,  /* cu_seqlens inconsistent (host check, or reported by the device) */
   KDA_ERR_CUDA = -6,     /* a CUDA runtime call or kernel launch failed */
   KDA_ERR_TIMEOUT = -7,  /* a kernel gave up a bounded wait and skipped its work */
-  KDA_ERR_SCRATCH = -8   /* kda_chunk_fwd_static: the call needs more scratch than
-                            KDA_STATIC_SCRATCH_BYTES; nothing was launched */
+  KDA_ERR_SCRATCH = -8,  /* kda_chunk_fwd_static: the call needs more scratch than
+                            KDA_STATIC_SCRATCH_BYTES, kda_mla_decode: the workspace is too
+                            small; nothing was launched */
+  KDA_ERR_PAGE = -9,     /* a position of the paged cache has no page in range (reported by
+                            the device) */
+  KDA_ERR_TREE = -10     /* a row of ancestor bits is not a path (reported by the device) */
 } kda_status;
 
 /*
@@ -393,10 +397,79 @@ int kda_decode_tokens(const void* q, const void* k, const void* v, const void* l
                       cudaStream_t stream);
 
 /*
+ * kda_decode_tree - the outputs of kda_decode_tokens for a TREE of new tokens per sequence,
+ * the state read and left as it is (verification of drafted tokens: the accepted path is
+ * then applied with kda_decode_tokens).
+ *
+ * Token r's output is what the recurrence gives after the tokens of its path, in order,
+ * from the sequence's state:  S <- (I - beta k k^T) Diag(alpha) S + beta k v^T over the
+ * path, o_r = S^T q_r. Computed in the chunk form (fp32) with "earlier token" replaced by
+ * "ancestor", so a chain equals kda_decode_tokens in real arithmetic, not bit for bit.
+ *
+ * Arguments: as kda_decode_tokens, but
+ *   state   [n_seqs, n_heads, 128, 128] fp32, read only
+ *   tree    [n_seqs, n_tokens] int32 on the device: bit i of tree[n][r] is set if token i is
+ *           an ancestor of token r, or r itself; parents come before their children. NULL: a
+ *           chain, every token the parent of the next. A row that is not its parent's row and
+ *           its own bit (the parent: the highest bit below r) is taken by its parent alone and
+ *           flagged (KDA_ERR_TREE from kda_device_status).
+ * Returns KDA_OK or a negative kda_status.
+ */
+int kda_decode_tree(const void* q, const void* k, const void* v, const void* log_alpha,
+                    const void* beta, const float* state, const int32_t* tree, void* o,
+                    int32_t n_seqs, int32_t n_tokens, int32_t n_heads, kda_dtype qkv_dtype,
+                    kda_dtype gate_dtype, cudaStream_t stream);
+
+/*
+ * Latent attention (MLA), the global attention layers that alternate with KDA layers (Note,
+ * section "Working Out the Cache by Hand": 576 cached values per token and layer; Summary,
+ * section 5: no positional encoding). A token's keys and values come from one vector of
+ * KDA_MLA_LATENT = 512 values shared by all heads, cached beside KDA_MLA_SHARED = 64 key values
+ * that the heads share as they are. Per head, a key is 128 values expanded from the latent
+ * followed by the 64 shared ones, a value 128 expanded from the latent.
+ *
+ * The cache is paged: cache [n_pages, page_size, 576] bf16; row p of sequence n lies in page
+ * page_table[n][p / page_size], at row p % page_size. page_table is [n_seqs, max_pages] int32
+ * and cache_lens [n_seqs] int32, both on the device and read when the kernels run. cache_lens[n]
+ * counts the sequence's rows WITH its new tokens, in every call: append the new tokens, then
+ * attend, with the same array. Rows at and past cache_lens[n] are never used, whatever they
+ * hold; values before it must be finite. A page number outside [0, n_pages), or a length past
+ * max_pages * page_size, is kept in bounds and flagged (KDA_ERR_PAGE from kda_device_status).
+ * int32 arrays of these calls need 4-byte alignment only.
+ */
+#define KDA_MLA_LATENT 512
+#define KDA_MLA_SHARED 64
+
+/*
+ * kda_mla_append - normalise new tokens' latents and write them into the paged cache.
+ *
+ *     y = x[0:512] / sqrt(mean(x[0:512]^2) + eps) * norm_w,  cached row = [y, x[512:576]]
+ *
+ * Arguments:
+ *   x           [t_total, 576] bf16, rows x_stride elements apart (a multiple of 8, at least
+ *               576: x may be a slice of a wider projection output)
+ *   norm_w      [512] fp32, or NULL: the latents are cached as they are
+ *   eps         >= 0
+ *   cu_seqlens  [n_seqs + 1] int32 as kda_chunk_fwd (sequence n's new tokens), or NULL: n_seqs
+ *               equal runs of t_total / n_seqs tokens
+ *   cache_lens  lengths after the append: token i of the T_n new ones of sequence n is row
+ *               cache_lens[n] - T_n + i. A token whose row is negative or has no page is not
+ *               written and flagged.
+ *   latent      [t_total, 512] bf16 output of the normalised latents (the expanded form's
+ *               projection reads them), or NULL
+ * Two tokens of one call must not share a row. Returns KDA_OK or a negative kda_status.
+ */
+int kda_mla_append(const void* x, int64_t x_stride, const float* norm_w, float eps, void* cache,
+                   int64_t n_pages, int32_t page_size, const int32_t* page_table,
+                   int32_t max_pages, const int32_t* cache_lens, const int32_t* cu_seqlens,
+                   int32_t n_seqs, int64_t t_total, void* latent, cudaStream_t stream);
+
+/*
  * kda_device_status - read and clear the library's device-side error word.
  * Synchronises `stream`. Returns KDA_OK, KDA_ERR_SEQLENS (a kernel saw
  * cu_seqlens that were not monotone or ran past t_total, and clamped them),
- * KDA_ERR_TIMEOUT (a kernel gave up a bounded wait), or KDA_ERR_CUDA.
+ * KDA_ERR_TIMEOUT (a kernel gave up a bounded wait), KDA_ERR_PAGE, KDA_ERR_TREE, or
+ * KDA_ERR_CUDA.
  *
  * The error word is one per GPU context and process, not per call or per stream:
  * every kernel of this library on the device ORs its errors into it, and any
