@@ -13,6 +13,7 @@ check their dtypes, shapes and contiguity, and pass raw pointers through.
 The latent-attention (MLA) layers that alternate with KDA layers, over a paged cache:
 
     mla_append(x, norm_w, cache, page_table, cache_lens, cu_seqlens)
+    o, lse = mla_prefill(q, k, k_shared, v, cu_seqlens)           # expanded form
 """
 
 from __future__ import annotations
@@ -436,6 +437,64 @@ def mla_append(x, norm_w, cache, page_table, cache_lens, cu_seqlens=None, latent
                                 _stream_ptr(dev))
     _native.check(st, "kda_mla_append")
     return latent
+
+
+def mla_prefill(q, k, k_shared, v, cu_seqlens=None, cu_seqlens_k=None, scale=None,
+                causal: bool = True, o=None, lse=None, output_lse: bool = False):
+    """Latent attention, expanded form: softmax attention of a packed batch.
+
+    q: [Tq, H, 192]; k, v: [Tk, H, 128] (expanded from the latents); k_shared: [Tk, 64], the
+    heads' shared key values, against q's last 64; all bf16, strided views allowed with a dense
+    last dimension. cu_seqlens: [N+1] int32 or None (one sequence); cu_seqlens_k: the keys'
+    where they differ (a prefix cached before): with causal a sequence's last query sees its
+    last key. scale: 1 / sqrt(192) by default. Returns (o, lse): o [Tq, H, 128] bf16, lse
+    [Tq, H] fp32 with output_lse (or into lse), else None.
+    """
+    lib = _native.load()
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [Tq, H, 192]")
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be [Tk, H, 128]")
+    dev, (Tq, H, _), Tk = q.device, q.shape, k.shape[0]
+    _need_rows(q, "q", torch.bfloat16, (Tq, H, D + MLA_SHARED), None)
+    _need_rows(k, "k", torch.bfloat16, (Tk, H, D), dev)
+    _need_rows(v, "v", torch.bfloat16, (Tk, H, D), dev)
+    _need_rows(k_shared, "k_shared", torch.bfloat16, (Tk, MLA_SHARED), dev)
+    N = 1
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be [N+1]")
+        N = cu_seqlens.numel() - 1
+        if cu_seqlens_k is None:
+            if Tk != Tq:
+                raise ValueError("cu_seqlens_k is needed where queries and keys differ in number")
+            cu_seqlens_k = cu_seqlens
+        _need(cu_seqlens_k, "cu_seqlens_k", torch.int32, (N + 1,), dev)
+    elif cu_seqlens_k is not None:
+        raise ValueError("cu_seqlens_k needs cu_seqlens")
+    if o is None:
+        o = torch.empty((Tq, H, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(o, "o", torch.bfloat16, (Tq, H, D), dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (Tq, H), dev)
+    elif output_lse:
+        lse = torch.empty((Tq, H), dtype=torch.float32, device=dev)
+    if scale is None:
+        scale = (D + MLA_SHARED) ** -0.5
+
+    def strides(t, width):
+        th = _row_stride(t, 1, width)
+        return _ptr(t), _row_stride(t, 0, H * th), th
+
+    with torch.cuda.device(dev):
+        st = lib.kda_mla_prefill(*strides(q, D + MLA_SHARED), *strides(k, D), _ptr(k_shared),
+                                 _row_stride(k_shared, 0, MLA_SHARED), *strides(v, D),
+                                 _ptr(cu_seqlens), _ptr(cu_seqlens_k), N, Tq, Tk, H, float(scale),
+                                 int(causal), _ptr(o), _ptr(lse), _stream_ptr(dev))
+    _native.check(st, "kda_mla_prefill")
+    return o, lse
 
 
 def device_status(device=None) -> int:

@@ -56,6 +56,8 @@ SIGNATURES = {
     "kda_decode_tree": [_P, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, ctypes.c_int,
                         ctypes.c_int, _P],
     "kda_mla_append": [_P, _I64, _P, _F32, _P, _I64, _I32, _P, _I32, _P, _P, _I32, _I64, _P, _P],
+    "kda_mla_prefill": [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _I32,
+                        _I64, _I64, _I32, _F32, _I32, _P, _P, _P],
     "kda_testing_chunk_fwd_stall": [_P, _P, _P, _P, _P, _P, _I64, _I32, _P, _P, _I32, ctypes.c_uint32,
                                     _P],
     "kda_device_status": [_P],

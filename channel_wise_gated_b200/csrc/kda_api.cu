@@ -19,6 +19,7 @@
 #include "kda_decode_tree.cuh"
 #include "kda_dplr_simt.cuh"
 #include "kda_mla_append.cuh"
+#include "kda_mla_prefill.cuh"
 #include "kda_segment.cuh"
 
 // Scratch of kda_chunk_fwd_static, for callers that cannot allocate device memory:
@@ -356,6 +357,41 @@ int launch_decode_tree(const void* q, const void* k, const void* v, const void* 
 static_assert(KDA_DECODE_MAX_TOKENS == kda::TREE_MAX_TOKENS, "token limit of the ABI and the kernel");
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// View of a bf16 tensor with dimensions dims[0] (dense) .. dims[rank-1] and byte strides, in
+// boxes with 128-byte rows, 128-byte swizzle. A box may be larger than the tensor: what lies
+// outside reads as zero.
+bool encode_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
+                 const uint64_t* strides, const uint32_t* box) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], es[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    es[i] = 1;
+    if (i > 0) st[i - 1] = strides[i - 1];
+  }
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), d, st,
+             b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A [tokens, heads, width] tensor with a dense last dimension, in boxes of 128 tokens of one
+// head and 64 columns.
+bool encode_heads(CUtensorMap* m, const void* base, uint64_t width, int32_t heads, int64_t tokens,
+                  int64_t stride_t, int64_t stride_h) {
+  const uint64_t dims[3] = {width, (uint64_t)heads, (uint64_t)tokens};
+  const uint64_t strides[2] = {(uint64_t)stride_h * 2, (uint64_t)stride_t * 2};
+  const uint32_t box[3] = {64, 1, 128};
+  return encode_bf16(m, base, 3, dims, strides, box);
+}
+
+// Element strides of a tensor with a dense last dimension: multiples of 16 bytes, below 2^40.
+bool stride_ok(int64_t s, int64_t least) {
+  return s >= least && (s & 7) == 0 && s < ((int64_t)1 << 38);
+}
 
 // The paged latent cache of the mla entry points: sizes and pointers (the table's and the
 // lengths' contents are checked by the kernels).
@@ -730,6 +766,64 @@ int kda_mla_append(const void* x, int64_t x_stride, const float* norm_w, float e
       static_cast<const __nv_bfloat16*>(x), x_stride, norm_w, eps, static_cast<__nv_bfloat16*>(cache),
       n_pages, page_size, page_table, max_pages, cache_lens, cu_seqlens, n_seqs, t_total,
       static_cast<__nv_bfloat16*>(latent));
+  return launch_status();
+}
+
+int kda_mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
+                    int64_t k_stride_t, int64_t k_stride_h, const void* k_shared,
+                    int64_t ks_stride_t, const void* v, int64_t v_stride_t, int64_t v_stride_h,
+                    const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int32_t n_seqs,
+                    int64_t tq_total, int64_t tk_total, int32_t n_heads, float scale,
+                    int32_t causal, void* o, float* lse, cudaStream_t stream) {
+  using namespace kda::mla::pf;
+  constexpr int DQ = kda::D + kda::mla::SHARED_K;
+  constexpr int64_t MOST = INT32_MAX - 4096;   // (32-bit token coordinates of the copies)
+  if (n_seqs <= 0 || n_heads <= 0 || tq_total < 0 || tk_total < 0 || tq_total > MOST || tk_total > MOST ||
+      !(scale > 0.f && scale < 1e30f))
+    return KDA_ERR_SHAPE;
+  if (!stride_ok(q_stride_t, DQ) || !stride_ok(q_stride_h, DQ) || !stride_ok(k_stride_t, kda::D) ||
+      !stride_ok(k_stride_h, kda::D) || !stride_ok(ks_stride_t, kda::mla::SHARED_K) ||
+      !stride_ok(v_stride_t, kda::D) || !stride_ok(v_stride_h, kda::D))
+    return KDA_ERR_SHAPE;
+  if ((cu_seqlens_q == nullptr) != (cu_seqlens_k == nullptr) || (cu_seqlens_q == nullptr && n_seqs != 1))
+    return KDA_ERR_SEQLENS;
+  const int64_t tiles = cu_seqlens_q == nullptr ? (tq_total + PAIR - 1) / PAIR : tq_total / PAIR + n_seqs;
+  if (tiles * n_heads > (int64_t)INT32_MAX) return KDA_ERR_SHAPE;
+  if (tq_total == 0) return KDA_OK;
+  if (!q || !o || (tk_total > 0 && (!k || !k_shared || !v))) return KDA_ERR_NULL;
+  const void* ptrs[] = {q, k, k_shared, v, o};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return KDA_ERR_ALIGN;
+  if (!aligned4(cu_seqlens_q) || !aligned4(cu_seqlens_k) || !aligned4(lse)) return KDA_ERR_ALIGN;
+  CUtensorMap mq, mk, ms, mv;
+  memset(&mk, 0, sizeof(mk));   // (without keys no kernel touches the maps)
+  memset(&ms, 0, sizeof(ms));
+  memset(&mv, 0, sizeof(mv));
+  bool ok = encode_heads(&mq, q, DQ, n_heads, tq_total, q_stride_t, q_stride_h);
+  if (tk_total > 0) {
+    const uint64_t dims[2] = {(uint64_t)kda::mla::SHARED_K, (uint64_t)tk_total};
+    const uint64_t strides[1] = {(uint64_t)ks_stride_t * 2};
+    const uint32_t box[2] = {64, 128};
+    ok = ok && encode_heads(&mk, k, kda::D, n_heads, tk_total, k_stride_t, k_stride_h) &&
+         encode_heads(&mv, v, kda::D, n_heads, tk_total, v_stride_t, v_stride_h) &&
+         encode_bf16(&ms, k_shared, 2, dims, strides, box);
+  }
+  if (!ok || cudaFuncSetAttribute(kda_mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)SMEM_BYTES) != cudaSuccess)
+    return KDA_ERR_CUDA;
+  Args a;
+  a.cu_q = cu_seqlens_q;
+  a.cu_k = cu_seqlens_k;
+  a.n_seqs = n_seqs;
+  a.n_heads = n_heads;
+  a.tiles = (int)tiles;
+  a.tq = tq_total;
+  a.tk = tk_total;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.scale = scale;
+  a.causal = causal != 0;
+  kda_mla_prefill_kernel<<<(unsigned)(tiles * n_heads), THREADS, SMEM_BYTES, stream>>>(mq, mk, ms, mv, a);
   return launch_status();
 }
 

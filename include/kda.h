@@ -465,6 +465,41 @@ int kda_mla_append(const void* x, int64_t x_stride, const float* norm_w, float e
                    int32_t n_seqs, int64_t t_total, void* latent, cudaStream_t stream);
 
 /*
+ * kda_mla_prefill - the expanded form: softmax attention over a packed batch of sequences.
+ *
+ *     s_ij = scale * (q_i[0:128] . k_j + q_i[128:192] . k_shared_j)
+ *     o_i = sum_j softmax_j(s_i) v_j,   lse_i = log sum_j e^{s_ij}
+ *
+ * over the keys j of i's sequence and, if causal, not after i, where a sequence's last query
+ * stands at its last key (with fewer queries than keys the queries are the newest tokens: the
+ * next part of a prompt after a prefix that is already cached). Without causal a call covers an
+ * earlier part of the context; two parts' outputs join by their lse. A row that sees no key gets
+ * o = 0 and lse = -inf.
+ *
+ * Arguments (bf16; the last dimension dense, other strides in elements and multiples of 8, so
+ * that k and v may be the halves of one projection's output):
+ *   q         [tq_total, n_heads, 192]
+ *   k, v      [tk_total, n_heads, 128]
+ *   k_shared  [tk_total, 64], shared by the heads
+ *   cu_seqlens_q, cu_seqlens_k   [n_seqs + 1] int32 each (the same array where queries and keys
+ *             are the same tokens), or both NULL: one sequence of tq_total queries and tk_total
+ *             keys. Bad contents are clamped and flagged (KDA_ERR_SEQLENS).
+ *   scale     > 0
+ *   o         [tq_total, n_heads, 128] bf16 output, dense
+ *   lse       [tq_total, n_heads] fp32 output (natural logarithm), or NULL
+ * Values must be finite: a NaN or infinity in a key or value that a row does not see may still
+ * reach it when both belong to one sequence; other sequences are not affected.
+ * Precision: bf16 operands, fp32 products, maxima and sums; the weights are rounded to bf16
+ * for the second product. Returns KDA_OK or a negative kda_status.
+ */
+int kda_mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
+                    int64_t k_stride_t, int64_t k_stride_h, const void* k_shared,
+                    int64_t ks_stride_t, const void* v, int64_t v_stride_t, int64_t v_stride_h,
+                    const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int32_t n_seqs,
+                    int64_t tq_total, int64_t tk_total, int32_t n_heads, float scale,
+                    int32_t causal, void* o, float* lse, cudaStream_t stream);
+
+/*
  * kda_device_status - read and clear the library's device-side error word.
  * Synchronises `stream`. Returns KDA_OK, KDA_ERR_SEQLENS (a kernel saw
  * cu_seqlens that were not monotone or ran past t_total, and clamped them),
