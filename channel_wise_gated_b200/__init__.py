@@ -13,7 +13,8 @@ check their dtypes, shapes and contiguity, and pass raw pointers through.
 The latent-attention (MLA) layers that alternate with KDA layers, over a paged cache:
 
     mla_append(x, norm_w, cache, page_table, cache_lens, cu_seqlens)
-    o, lse = mla_prefill(q, k, k_shared, v, cu_seqlens)           # expanded form
+    o, lse = mla_prefill(q, k, k_shared, v, cu_seqlens)               # expanded form
+    o, lse = mla_decode(q, cache, page_table, cache_lens, tree=None)  # absorbed form
 """
 
 from __future__ import annotations
@@ -494,6 +495,55 @@ def mla_prefill(q, k, k_shared, v, cu_seqlens=None, cu_seqlens_k=None, scale=Non
                                  _ptr(cu_seqlens), _ptr(cu_seqlens_k), N, Tq, Tk, H, float(scale),
                                  int(causal), _ptr(o), _ptr(lse), _stream_ptr(dev))
     _native.check(st, "kda_mla_prefill")
+    return o, lse
+
+
+def mla_decode(q, cache, page_table, cache_lens, tree=None, scale=None, o=None, lse=None,
+               output_lse: bool = False, workspace=None):
+    """Latent attention, absorbed form: 1 to 16 new tokens per sequence over the paged cache.
+
+    q: [N, t, H, 576] bf16 (queries multiplied into the latent space, then their 64 shared
+    values); cache: [n_pages, page_size, 576] bf16, page_size a multiple of 8; page_table: [N,
+    max_pages] int32; cache_lens: [N] int32, lengths with the t new tokens, which mla_append has
+    written; tree: [N, t] int32 ancestor bits as decode_tree, or None (a chain). scale:
+    1 / sqrt(192) by default. workspace: uint8 of kda_mla_decode_workspace_size bytes, allocated
+    here if None; calls that may overlap need one each. Returns (o, lse): o [N, t, H, 512] bf16
+    in the latent space, lse [N, t, H] fp32 with output_lse (or into lse), else None.
+    """
+    lib = _native.load()
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.shape[3] != MLA_WIDTH:
+        raise ValueError("q must be [N, t, H, 576]")
+    N, t, H, _ = q.shape
+    if not 1 <= t <= _native.KDA_DECODE_MAX_TOKENS:
+        raise ValueError(f"t must be in 1..{_native.KDA_DECODE_MAX_TOKENS}")
+    _need(q, "q", torch.bfloat16)
+    dev = q.device
+    n_pages, page_size, max_pages = _paged_cache(cache, page_table, cache_lens, N, dev)
+    if page_size % 8:
+        raise ValueError("page_size must be a multiple of 8")
+    if tree is not None:
+        _need(tree, "tree", torch.int32, (N, t), dev)
+    if o is None:
+        o = torch.empty((N, t, H, MLA_LATENT), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(o, "o", torch.bfloat16, (N, t, H, MLA_LATENT), dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (N, t, H), dev)
+    elif output_lse:
+        lse = torch.empty((N, t, H), dtype=torch.float32, device=dev)
+    if scale is None:
+        scale = (D + MLA_SHARED) ** -0.5
+    with torch.cuda.device(dev):
+        if workspace is None:
+            workspace = torch.empty(lib.kda_mla_decode_workspace_size(t, H), dtype=torch.uint8,
+                                    device=dev)
+        else:
+            _need(workspace, "workspace", torch.uint8, None, dev)
+        st = lib.kda_mla_decode(_ptr(q), _ptr(cache), n_pages, page_size, _ptr(page_table),
+                                max_pages, _ptr(cache_lens), _ptr(tree), N, t, H, float(scale),
+                                _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel(),
+                                _stream_ptr(dev))
+    _native.check(st, "kda_mla_decode")
     return o, lse
 
 

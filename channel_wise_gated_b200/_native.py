@@ -58,6 +58,9 @@ SIGNATURES = {
     "kda_mla_append": [_P, _I64, _P, _F32, _P, _I64, _I32, _P, _I32, _P, _P, _I32, _I64, _P, _P],
     "kda_mla_prefill": [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _I32,
                         _I64, _I64, _I32, _F32, _I32, _P, _P, _P],
+    "kda_mla_decode_workspace_size": [_I32, _I32],
+    "kda_mla_decode": [_P, _P, _I64, _I32, _P, _I32, _P, _P, _I32, _I32, _I32, _F32, _P, _P, _P,
+                       ctypes.c_size_t, _P],
     "kda_testing_chunk_fwd_stall": [_P, _P, _P, _P, _P, _P, _I64, _I32, _P, _P, _I32, ctypes.c_uint32,
                                     _P],
     "kda_device_status": [_P],
@@ -87,7 +90,8 @@ def load(path: str = LIB_PATH):
         fn = getattr(lib, name)
         fn.argtypes = argtypes
         fn.restype = {"kda_status_string": ctypes.c_char_p,
-                      "kda_chunk_fwd_workspace_size": ctypes.c_size_t}.get(name, ctypes.c_int)
+                      "kda_chunk_fwd_workspace_size": ctypes.c_size_t,
+                      "kda_mla_decode_workspace_size": ctypes.c_size_t}.get(name, ctypes.c_int)
     _lib = lib
     return lib
 

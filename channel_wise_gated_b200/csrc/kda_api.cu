@@ -19,6 +19,7 @@
 #include "kda_decode_tree.cuh"
 #include "kda_dplr_simt.cuh"
 #include "kda_mla_append.cuh"
+#include "kda_mla_decode.cuh"
 #include "kda_mla_prefill.cuh"
 #include "kda_segment.cuh"
 
@@ -386,6 +387,18 @@ bool encode_heads(CUtensorMap* m, const void* base, uint64_t width, int32_t head
   const uint64_t strides[2] = {(uint64_t)stride_h * 2, (uint64_t)stride_t * 2};
   const uint32_t box[3] = {64, 1, 128};
   return encode_bf16(m, base, 3, dims, strides, box);
+}
+
+// Row groups of the absorbed form: `rows` (token, head) rows of a sequence in the fewest items
+// of at most 64, of equal size up to padding.
+void mla_decode_groups(int32_t rows, int& groups, int& rb) {
+  groups = (rows + kda::mla::dec::ROWS - 1) / kda::mla::dec::ROWS;
+  rb = ((rows + groups - 1) / groups + 15) / 16 * 16;
+  groups = (rows + rb - 1) / rb;
+}
+
+size_t mla_decode_workspace(int sms, int rb) {
+  return (size_t)2 * sms * rb * (kda::mla::LATENT + 2) * sizeof(float);
 }
 
 // Element strides of a tensor with a dense last dimension: multiples of 16 bytes, below 2^40.
@@ -825,6 +838,74 @@ int kda_mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const
   a.causal = causal != 0;
   kda_mla_prefill_kernel<<<(unsigned)(tiles * n_heads), THREADS, SMEM_BYTES, stream>>>(mq, mk, ms, mv, a);
   return launch_status();
+}
+
+size_t kda_mla_decode_workspace_size(int32_t n_tokens, int32_t n_heads) {
+  if (n_tokens <= 0 || n_tokens > KDA_DECODE_MAX_TOKENS || n_heads <= 0 || n_heads > INT32_MAX / 64) return 0;
+  int groups, rb;
+  mla_decode_groups(n_tokens * n_heads, groups, rb);
+  return mla_decode_workspace(device_sms(), rb);
+}
+
+int kda_mla_decode(const void* q, const void* cache, int64_t n_pages, int32_t page_size,
+                   const int32_t* page_table, int32_t max_pages, const int32_t* cache_lens,
+                   const int32_t* tree, int32_t n_seqs, int32_t n_tokens, int32_t n_heads,
+                   float scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                   cudaStream_t stream) {
+  using namespace kda::mla;
+  using namespace kda::mla::dec;
+  if (n_seqs <= 0 || n_heads <= 0 || n_tokens <= 0 || n_tokens > KDA_DECODE_MAX_TOKENS ||
+      (int64_t)n_seqs * n_tokens * n_heads > (int64_t)INT32_MAX - 64 || !(scale > 0.f && scale < 1e30f))
+    return KDA_ERR_SHAPE;
+  const int st = validate_cache(cache, n_pages, page_size, page_table, max_pages, cache_lens);
+  if (st != KDA_OK) return st;
+  if ((page_size & 7) != 0) return KDA_ERR_SHAPE;
+  if (!q || !o || !workspace) return KDA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(workspace) || !aligned4(tree) || !aligned4(lse))
+    return KDA_ERR_ALIGN;
+  const int sms = device_sms();
+  if (sms <= 0) return KDA_ERR_CUDA;
+  Args a;
+  a.rows = n_tokens * n_heads;
+  mla_decode_groups(a.rows, a.groups, a.rb);
+  if (workspace_bytes < mla_decode_workspace(sms, a.rb)) return KDA_ERR_SCRATCH;
+  a.page_table = page_table;
+  a.cache_lens = cache_lens;
+  a.tree = tree;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.part = static_cast<float*>(workspace);
+  a.n_seqs = n_seqs;
+  a.n_tokens = n_tokens;
+  a.n_heads = n_heads;
+  a.n_pages = (int)n_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.page_rows = std::min(page_size & -page_size, 64);
+  const int64_t line = (int64_t)n_seqs * a.groups * (((int64_t)max_pages * page_size + BN - 1) / BN);
+  a.grid = (int)std::min<int64_t>(sms, line);
+  a.scale = scale;
+  CUtensorMap mq, mc;
+  const uint64_t qd[3] = {64, (uint64_t)n_seqs * a.rows, WIDTH / 64}, qs[2] = {WIDTH * 2, 128};
+  const uint32_t qb[3] = {64, (uint32_t)a.rb, WIDTH / 64};
+  const uint64_t cd[4] = {64, 8, WIDTH / 64, (uint64_t)n_pages * page_size / 8}, cs[3] = {WIDTH * 2, 128, GROUP};
+  const uint32_t cb[4] = {64, 8, WIDTH / 64, (uint32_t)a.page_rows / 8};
+  if (!encode_bf16(&mq, q, 3, qd, qs, qb) || !encode_bf16(&mc, cache, 4, cd, cs, cb) ||
+      cudaFuncSetAttribute(kda_mla_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)smem_bytes(ROWS)) != cudaSuccess)
+    return KDA_ERR_CUDA;
+  kda_mla_decode_kernel<<<(unsigned)a.grid, THREADS, smem_bytes(a.rb), stream>>>(mq, mc, a);
+  if (launch_status() != KDA_OK) return KDA_ERR_CUDA;
+  if (a.grid > 1) {
+    const int64_t items = (int64_t)n_seqs * a.groups;
+    const int by_item = items <= a.grid - 1;
+    const int x = by_item ? (int)items : a.grid - 1;
+    const int per = std::min(a.rb, std::max(1, (x * a.rb + 4 * sms - 1) / (4 * sms)));
+    kda_mla_decode_join_kernel<<<dim3((unsigned)x, (unsigned)((a.rb + per - 1) / per)), JOIN_THREADS, 0, stream>>>(
+        a, by_item, per);
+    return launch_status();
+  }
+  return KDA_OK;
 }
 
 int kda_testing_chunk_fwd_stall(const void* q, const void* k, const void* v,

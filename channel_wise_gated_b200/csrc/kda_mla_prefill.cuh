@@ -26,12 +26,15 @@
 namespace kda {
 namespace mla {
 
-// Bounded wait of a role: false once the wait runs out (2 s) or another role has given up.
+// Bounded wait of a whole warp (the same answer in every lane): false once the wait runs out
+// (2 s) or another role has given up. `one` is the same for a single thread.
 struct Waiter {
   volatile int* abort_flag;
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-    if (sm100::mbar_try_wait(bar, parity)) return true;
-    return slow(bar, parity);
+    return __all_sync(0xffffffffu, one(bar, parity));
+  }
+  __device__ __forceinline__ bool one(uint64_t* bar, uint32_t parity) const {
+    return sm100::mbar_try_wait(bar, parity) || slow(bar, parity);
   }
   __device__ __forceinline__ bool slow(uint64_t* bar, uint32_t parity) const {
     const uint64_t t0 = sm100::globaltimer_ns();
@@ -228,7 +231,7 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
       }
       if (n_tiles > 1) issue_k(1);
       for (int j = 0; j < n_tiles && alive; ++j) {
-        if (j >= 1) alive = wait(&bars[B_VFREE], (j - 1) & 1);
+        if (j >= 1) alive = wait.one(&bars[B_VFREE], (j - 1) & 1);
         if (!alive) break;
         mbar_arrive_expect_tx(&bars[B_VFULL], V_BYTES);
         const int y = (int)(bk + (int64_t)j * BN);
@@ -236,7 +239,7 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
         tma_load_3d(sm + OFF_V + BLK, &map_v, 64, head, y, &bars[B_VFULL]);
         ++v_issued;
         if (j + 2 < n_tiles) {
-          alive = wait(&bars[B_KFREE + (j & 1)], (j >> 1) & 1);
+          alive = wait.one(&bars[B_KFREE + (j & 1)], (j >> 1) & 1);
           if (alive) issue_k(j + 2);
         }
       }

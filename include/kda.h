@@ -500,6 +500,41 @@ int kda_mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const
                     int32_t causal, void* o, float* lse, cudaStream_t stream);
 
 /*
+ * kda_mla_decode - the absorbed form: new tokens' queries against the paged latent cache, which
+ * is key (576 values) and value (the first 512) of every head at once.
+ *
+ *     s_rj = scale * q_r . c_j,   o_r = sum_j softmax_j(s_r) c_j[0:512]
+ *
+ * with q_r = [W_UK^T q_nope, q_shared] per (token, head) and o_r still to be taken through W_UV:
+ * plain projections on either side. The sequence's n_tokens newest rows (its new tokens,
+ * appended before) are cache_lens[n] - n_tokens .. cache_lens[n] - 1. A token sees every row
+ * before them and, of them, those of its bits.
+ *
+ * Arguments:
+ *   q        [n_seqs, n_tokens, n_heads, 576] bf16, n_tokens 1 .. KDA_DECODE_MAX_TOKENS
+ *   cache, n_pages, page_size, page_table, max_pages, cache_lens   as kda_mla_append; page_size
+ *            a multiple of 8. Length 0: o = 0, lse = -inf (an empty slot of the batch).
+ *   tree     [n_seqs, n_tokens] int32, bit i of tree[n][r]: token r sees the i-th of the newest
+ *            rows (for a tree of drafted tokens its ancestors and itself, as kda_decode_tree), or
+ *            NULL: a chain (0 .. r). Bits that reach before row 0 mean nothing.
+ *   scale    > 0
+ *   o        [n_seqs, n_tokens, n_heads, 512] bf16 output
+ *   lse      [n_seqs, n_tokens, n_heads] fp32 output (natural logarithm), or NULL
+ *   workspace, workspace_bytes   kda_mla_decode_workspace_size(n_tokens, n_heads) bytes on the
+ *            current device, 16-byte aligned (KDA_ERR_SCRATCH if less). Nothing in it has to be set; it must
+ *            stay untouched until the stream has passed the call: calls that may overlap on the
+ *            GPU need one each.
+ * Results do not depend on timing: the parts of a sequence are joined in a fixed order.
+ * Precision: as kda_mla_prefill. Returns KDA_OK or a negative kda_status.
+ */
+size_t kda_mla_decode_workspace_size(int32_t n_tokens, int32_t n_heads);
+int kda_mla_decode(const void* q, const void* cache, int64_t n_pages, int32_t page_size,
+                   const int32_t* page_table, int32_t max_pages, const int32_t* cache_lens,
+                   const int32_t* tree, int32_t n_seqs, int32_t n_tokens, int32_t n_heads,
+                   float scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                   cudaStream_t stream);
+
+/*
  * kda_device_status - read and clear the library's device-side error word.
  * Synchronises `stream`. Returns KDA_OK, KDA_ERR_SEQLENS (a kernel saw
  * cu_seqlens that were not monotone or ran past t_total, and clamped them),

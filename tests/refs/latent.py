@@ -28,9 +28,8 @@ def rmsnorm(x, w, eps):
 def cached_rows(cache, page_table, n, first, last):
     """Rows first .. last-1 of sequence n, [last - first, 576] in 64 bits."""
     ps = cache.shape[1]
-    return torch.stack([cache[int(page_table[n, p // ps]), p % ps].double()
-                        for p in range(first, last)]) if last > first else \
-        torch.zeros(0, cache.shape[2], dtype=torch.float64)
+    p = torch.arange(first, max(first, last))
+    return cache[page_table[n, p // ps].long(), p % ps].double()
 
 
 def attend(q, keys, values, scale):
