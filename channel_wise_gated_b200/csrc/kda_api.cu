@@ -869,6 +869,7 @@ int kda_mla_decode(const void* q, const void* cache, int64_t n_pages, int32_t pa
   a.rows = n_tokens * n_heads;
   mla_decode_groups(a.rows, a.groups, a.rb);
   if (workspace_bytes < mla_decode_workspace(sms, a.rb)) return KDA_ERR_SCRATCH;
+  a.cache = cache;
   a.page_table = page_table;
   a.cache_lens = cache_lens;
   a.tree = tree;
@@ -881,7 +882,7 @@ int kda_mla_decode(const void* q, const void* cache, int64_t n_pages, int32_t pa
   a.n_pages = (int)n_pages;
   a.page_size = page_size;
   a.max_pages = max_pages;
-  a.page_rows = std::min(page_size & -page_size, 64);
+  a.page_rows = std::min(page_size & -page_size, BN);
   const int64_t line = (int64_t)n_seqs * a.groups * (((int64_t)max_pages * page_size + BN - 1) / BN);
   a.grid = (int)std::min<int64_t>(sms, line);
   a.scale = scale;
@@ -892,18 +893,28 @@ int kda_mla_decode(const void* q, const void* cache, int64_t n_pages, int32_t pa
   const uint32_t cb[4] = {64, 8, WIDTH / 64, (uint32_t)a.page_rows / 8};
   if (!encode_bf16(&mq, q, 3, qd, qs, qb) || !encode_bf16(&mc, cache, 4, cd, cs, cb) ||
       cudaFuncSetAttribute(kda_mla_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem_bytes(ROWS)) != cudaSuccess)
+                           (int)SMEM_MOST) != cudaSuccess)
     return KDA_ERR_CUDA;
   kda_mla_decode_kernel<<<(unsigned)a.grid, THREADS, smem_bytes(a.rb), stream>>>(mq, mc, a);
   if (launch_status() != KDA_OK) return KDA_ERR_CUDA;
   if (a.grid > 1) {
+    // (the join's launch overlaps the end of the main kernel, which it waits for itself)
     const int64_t items = (int64_t)n_seqs * a.groups;
     const int by_item = items <= a.grid - 1;
-    const int x = by_item ? (int)items : a.grid - 1;
-    const int per = std::min(a.rb, std::max(1, (x * a.rb + 4 * sms - 1) / (4 * sms)));
-    kda_mla_decode_join_kernel<<<dim3((unsigned)x, (unsigned)((a.rb + per - 1) / per)), JOIN_THREADS, 0, stream>>>(
-        a, by_item, per);
-    return launch_status();
+    const bool alone = items * 8 > a.grid;
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)(by_item ? items : a.grid - 1),
+                     (unsigned)(alone ? (a.rb + JOIN_WARPS - 1) / JOIN_WARPS : a.rb));
+    c.blockDim = dim3(JOIN_THREADS);
+    c.stream = stream;
+    c.attrs = &early;
+    c.numAttrs = 1;
+    const cudaError_t e = alone ? cudaLaunchKernelEx(&c, kda_mla_decode_join_kernel<true>, a, by_item)
+                                : cudaLaunchKernelEx(&c, kda_mla_decode_join_kernel<false>, a, by_item);
+    if (e != cudaSuccess || launch_status() != KDA_OK) return KDA_ERR_CUDA;
   }
   return KDA_OK;
 }

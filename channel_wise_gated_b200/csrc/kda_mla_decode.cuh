@@ -10,13 +10,13 @@
 // Bound: 1,152 bytes per cached token, read once for up to 64 (token, head) rows, against
 // 2 (576 + 512) flops per row: HBM up to about 100 rows.
 //
-// A tile of 64 keys is copied once into shared memory and serves both products from there: as
-// the K-major B operand of S = Q K^T (64 x 64), and, read the other way round, as the MN-major A
+// A tile of 32 keys is copied once into shared memory and serves both products from there: as
+// the K-major B operand of S = Q K^T (64 x 32), and, read the other way round, as the MN-major A
 // operand of O^T = V^T P^T, whose 512 latents fill four accumulators of 128 lanes with the rows
 // as columns. That way few rows cost few columns (a 64-row O would always cost 128 lanes), and
 // P needs no transpose: a softmax warp writes its rows as the K-major B operand.
 // Warps 0-3: softmax of rows 16w .. 16w+15 of S, rescaling and output of latents 32w .. + 31 of
-// every accumulator; warp 4: copies; warp 5: products.
+// every accumulator; warp 4: copies; warps 5 and 6: the two products.
 //
 // The work of all sequences is one line of tiles, cut into equal runs, one per CTA, so ragged
 // lengths and few long sequences fill the GPU alike. A run covers parts of one or more
@@ -33,23 +33,36 @@ namespace kda {
 namespace mla {
 namespace dec {
 
-constexpr int BN = 64;                                  // keys per tile
+constexpr int BN = 32;                                  // keys per tile
 constexpr int ROWS = 64;                                // (token, head) rows of one item at most
-constexpr int THREADS = 192;
+constexpr int THREADS = 224;
 constexpr uint32_t GROUP = 8 * WIDTH * 2;               // 8 cached rows: nine 1 KiB swizzle atoms
-constexpr uint32_t STAGE = BN / 8 * GROUP;              // 73,728 bytes
+constexpr uint32_t STAGE = BN / 8 * GROUP;              // 36,864 bytes
+constexpr int MAX_STAGES = 5;
+constexpr int FETCH = 4;                                // tiles from a piece's L2 prefetch to its copy
 constexpr int MIN_TILES = 2;                            // a CTA's run is at least this long
-enum { B_KVFULL = 0, B_KVFREE = 2, B_SFULL = 4, B_PFULL = 6, B_PVDONE, B_QFULL, B_QFREE, B_OFREE, B_DRAIN, N_BARS };
-constexpr uint32_t TM_O = 0, TM_S = 256;                // four accumulators 64 columns apart; S twice
+enum { B_KVFULL = 0, B_KVFREE = MAX_STAGES, B_SFULL = 2 * MAX_STAGES, B_PFULL = B_SFULL + 8, B_PVDONE = B_PFULL + 2,
+       B_QFULL = B_PVDONE + 2, B_QFREE, B_OFREE, B_DRAIN, N_BARS = B_DRAIN + 2 };
+constexpr uint32_t TM_O = 0, TM_S = 256;                // four accumulators 64 columns apart; eight S
 
-// Shared memory: Q, two stages, P, barriers, the rows' factors, scratch of the search.
+// Shared memory: Q, the stages (as many as fit, 5 up to 32 rows, else 4), P twice, barriers, the
+// rows' factors.
+constexpr uint32_t SMEM_MOST = 232448 - 1024;           // (less the static part)
+__host__ __device__ constexpr uint32_t p_bytes(int rb) { return (uint32_t)rb * BN * 2; }
 __host__ __device__ constexpr uint32_t off_kv(int rb) { return (uint32_t)rb * WIDTH * 2; }
-__host__ __device__ constexpr uint32_t off_p(int rb) { return off_kv(rb) + 2 * STAGE; }
-__host__ __device__ constexpr uint32_t off_bar(int rb) { return off_p(rb) + (uint32_t)rb * BN * 2; }
-__host__ __device__ constexpr uint32_t smem_bytes(int rb) { return off_bar(rb) + 128 + 2 * ROWS * 4 + 64 + 1024; }
-static_assert(smem_bytes(ROWS) <= 232448 - 1024, "shared memory of one CTA");
+constexpr uint32_t TAIL = 256 + 2 * ROWS * 4 + 1024;    // barriers, factors, alignment
+__host__ __device__ constexpr int stages_of(int rb) {
+  return off_kv(rb) + MAX_STAGES * STAGE + 2 * p_bytes(rb) + TAIL <= SMEM_MOST ? MAX_STAGES : MAX_STAGES - 1;
+}
+__host__ __device__ constexpr uint32_t off_p(int rb) { return off_kv(rb) + stages_of(rb) * STAGE; }
+__host__ __device__ constexpr uint32_t off_bar(int rb) { return off_p(rb) + 2 * p_bytes(rb); }
+__host__ __device__ constexpr uint32_t smem_bytes(int rb) { return off_bar(rb) + TAIL; }
+static_assert(smem_bytes(16) <= SMEM_MOST && smem_bytes(32) <= SMEM_MOST && smem_bytes(48) <= SMEM_MOST &&
+                  smem_bytes(64) <= SMEM_MOST && N_BARS * 8 <= 256,
+              "shared memory of one CTA");
 
 struct Args {
+  const void* cache;
   const int32_t* page_table;
   const int32_t* cache_lens;
   const int32_t* tree;
@@ -61,7 +74,7 @@ struct Args {
   int groups;           // items per sequence
   int rb;               // rows of an item, padded: 16, 32, 48 or 64
   int n_pages, page_size, max_pages;
-  int page_rows;        // rows per copy: the largest power of two up to 64 that divides page_size
+  int page_rows;        // rows per copy: the largest power of two up to a tile's that divides page_size
   int grid;             // CTAs of the main kernel
   float scale;
 };
@@ -184,7 +197,8 @@ kda_mla_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
   extern __shared__ unsigned char dec_smem_raw[];
   unsigned char* sm = dec_smem_raw + ((1024u - (smem_u32(dec_smem_raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + off_bar(a.rb));
-  float* s_fac = reinterpret_cast<float*>(sm + off_bar(a.rb) + 128);   // a factor per row
+  float* s_fac = reinterpret_cast<float*>(sm + off_bar(a.rb) + 256);   // a factor per row
+  const int stages = stages_of(a.rb);
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ int64_t s_sums[THREADS / 32], s_found[2];
@@ -203,9 +217,10 @@ kda_mla_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
   int64_t begin, end, first_at;
   locate<THREADS>(a, s_sums, s_found, blockIdx.x, workers, begin, end, n_at, first_at);
   if (begin >= end) return;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the join waits for this kernel's end)
   if (tid == 0) {
     s_abort = 0;
-    for (int i = 0; i < N_BARS; ++i) mbar_init(&bars[i], i == B_PFULL || i == B_OFREE ? 128 : 1);
+    for (int i = 0; i < N_BARS; ++i) mbar_init(&bars[i], i == B_PFULL || i == B_PFULL + 1 || i == B_OFREE ? 128 : 1);
     fence_mbar_init();
   }
   if (warp == 4) {
@@ -226,30 +241,58 @@ kda_mla_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
 
   if (warp == 4) {
     // ---- copies: lane c brings the c-th piece of page_rows rows of a tile ----
+    // The stages that a tile's products do not hold cover about 110 KiB of copies in flight per
+    // SM, too little for HBM's latency under load (2.7 us a tile, 4.0 TB/s): so every piece is
+    // brought into L2 FETCH tiles ahead of its copy, along with reading its page's number.
     const int pieces = BN / a.page_rows;
-    int it = 0, sg = 0;
-    bool alive = true;
-    for (; more && alive; more = w.next(a), ++sg) {
-      for (int i = w.t0; i < w.t1 && alive; ++i, ++it) {
-        const int pos = i * BN + lane * a.page_rows;
-        int row8 = 0;
-        const bool mine = lane < pieces && pos < w.len;
-        if (mine) {
+    Walk wa = w;
+    int ia = w.t0;
+    bool a_left = more;
+    // the cursor's piece of this lane: its first row over 8, or -1; then a tile further
+    auto look = [&](bool fetch) {
+      int row8 = -1;
+      if (a_left) {
+        const int pos = ia * BN + lane * a.page_rows;
+        if (lane < pieces && pos < wa.len) {
           const int pi = pos / a.page_size;
-          int page = a.page_table[(int64_t)w.n * a.max_pages + pi];
+          int page = a.page_table[(int64_t)wa.n * a.max_pages + pi];
           if (page < 0 || page >= a.n_pages) {
             flag_error(DEVERR_PAGE);
             page = 0;
           }
           row8 = (int)(((int64_t)page * a.page_size + (pos - pi * a.page_size)) >> 3);
+          if (fetch)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                             reinterpret_cast<const unsigned char*>(a.cache) + (int64_t)row8 * GROUP),
+                         "r"((uint32_t)a.page_rows * (WIDTH * 2))
+                         : "memory");
         }
-        const int count = __popc(__ballot_sync(0xffffffffu, mine));
-        uint64_t* full = &bars[B_KVFULL + (it & 1)];
-        if (it >= 2) alive = wait(&bars[B_KVFREE + (it & 1)], ((it >> 1) - 1) & 1);
+        if (++ia == wa.t1) {
+          a_left = wa.next(a);
+          ia = wa.t0;
+        }
+      }
+      return row8;
+    };
+    int queue[FETCH];
+#pragma unroll
+    for (int k = 0; k < FETCH; ++k) queue[k] = look(k >= 2);
+    int it = 0, sg = 0, st = 0, round = 0;   // tile, item, stage and its use
+    bool alive = true;
+    for (; more && alive; more = w.next(a), ++sg) {
+      for (int i = w.t0; i < w.t1 && alive; ++i, ++it, st = st + 1 == stages ? 0 : st + 1, round += st == 0) {
+        const int row8 = queue[0];
+#pragma unroll
+        for (int k = 1; k < FETCH; ++k) queue[k - 1] = queue[k];
+        queue[FETCH - 1] = look(true);
+        const int count = __popc(__ballot_sync(0xffffffffu, row8 >= 0));
+        uint64_t* full = &bars[B_KVFULL + st];
+        if (round > 0) alive = wait(&bars[B_KVFREE + st], (round - 1) & 1);
         if (!alive) break;
         if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)count * a.page_rows * (WIDTH * 2));
         __syncwarp();
-        if (mine) tma_load_4d(sm + off_kv(a.rb) + (it & 1) * STAGE + lane * (a.page_rows / 8) * GROUP, &map_c, row8, full);
+        if (row8 >= 0)
+          tma_load_4d(sm + off_kv(a.rb) + st * STAGE + lane * (a.page_rows / 8) * GROUP, &map_c, row8, full);
         if (i == w.t0) {   // (after the item's first keys, which need not wait for the item before)
           if (sg > 0) alive = wait(&bars[B_QFREE], (sg - 1) & 1);
           if (alive && lane == 0) {
@@ -261,75 +304,91 @@ kda_mla_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
       if (!alive) break;
     }
     if (!alive && lane == 0) {   // (sg: Q loads issued so far lie at or below it)
-      for (int j = max(0, it - 1); j <= it; ++j) settle_bar(&bars[B_KVFULL + (j & 1)], (j >> 1) & 1);
+      for (int j = max(0, it + 1 - stages); j <= it; ++j)
+        settle_bar(&bars[B_KVFULL + j % stages], (j / stages) & 1);
       settle_bar(&bars[B_QFULL], sg & 1);
     }
   } else if (warp == 5) {
-    // ---- products ----
+    // ---- S = Q K^T ----
+    // The two products have a warp each: from one, in any order, every wait between them left
+    // the tensor cores idle for 400 to 500 cycles (the barriers share the port of shared memory
+    // that the operands keep busy), 1,000 of a tile's 2,400. S goes on into eight buffers: the
+    // one a tile takes was read when the tile's stage came free.
     const uint32_t sb = smem_u32(sm);
-    const uint32_t idesc_s = idesc_bf16(64, BN, 0, 0), idesc_pv = idesc_bf16(128, (uint32_t)a.rb, 1, 0);
+    const uint32_t idesc = idesc_bf16(64, BN, 0, 0);
     const uint64_t q0 = make_sdesc(sb, 16, 1024, SWZ_128B);
-    const uint64_t p0 = make_sdesc(sb + off_p(a.rb), 16, 1024, SWZ_128B);
     const uint32_t q_blk = ((uint32_t)a.rb * 128) >> 4;
-    int it = 0, sg = 0;
+    int it = 0, sg = 0, st = 0, round = 0;
     bool alive = true;
-    // O^T += V^T P^T of tile i of the item, number `t` of the run
-    auto pv = [&](int i, int t) {
-      if (i == w.t0 && sg > 0) alive = alive && wait(&bars[B_OFREE], (sg - 1) & 1);
-      alive = alive && wait(&bars[B_PFULL], t & 1);
-      if (!alive) return;
-      tc_fence_after();
-      const int steps = min(BN / 16, (w.len - i * BN + 15) >> 4);
-      if (lane == 0) {
-        const uint64_t v0 = make_sdesc(sb + off_kv(a.rb) + (t & 1) * STAGE, 1024, GROUP, SWZ_128B);
-#pragma unroll 1
-        for (int kk = 0; kk < steps; ++kk)
-#pragma unroll
-          for (int mb = 0; mb < 4; ++mb)
-            umma_bf16(tmem + TM_O + mb * 64, v0 + ((kk * 2 * GROUP + mb * 2048) >> 4), p0 + ((kk * 32) >> 4),
-                      idesc_pv, (i > w.t0 || kk > 0) ? 1u : 0u);
-        umma_commit(&bars[B_KVFREE + (t & 1)]);
-        umma_commit(&bars[B_PVDONE]);
-      }
-    };
     for (; more && alive; more = w.next(a), ++sg) {
       alive = wait(&bars[B_QFULL], sg & 1);
-      for (int i = w.t0; i < w.t1 && alive; ++i, ++it) {
-        if (!(alive = wait(&bars[B_KVFULL + (it & 1)], (it >> 1) & 1))) break;
+      for (int i = w.t0; i < w.t1 && alive; ++i, ++it, st = st + 1 == stages ? 0 : st + 1, round += st == 0) {
+        if (!(alive = wait(&bars[B_KVFULL + st], round & 1))) break;
         const int valid = w.len - i * BN;
         if (valid < BN && (valid & 15)) {
           // rows behind the last key in its 16-row step (an earlier tile's, or nothing yet):
           // their weights of zero must meet zeros
           const int r1 = (valid + 15) & ~15;
-          unsigned char* st = sm + off_kv(a.rb) + (it & 1) * STAGE;
+          unsigned char* kv = sm + off_kv(a.rb) + st * STAGE;
           for (int k = lane; k < (r1 - valid) * (WIDTH / 8); k += 32) {
             const int r = valid + k / (WIDTH / 8), c = k % (WIDTH / 8);
-            *reinterpret_cast<uint4*>(st + (r >> 3) * GROUP + (c >> 3) * 1024 + (r & 7) * 128 + (c & 7) * 16) =
+            *reinterpret_cast<uint4*>(kv + (r >> 3) * GROUP + (c >> 3) * 1024 + (r & 7) * 128 + (c & 7) * 16) =
                 make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
           __syncwarp();
         }
         tc_fence_after();
-        if (lane == 0) {
-          const uint64_t k0 = make_sdesc(sb + off_kv(a.rb) + (it & 1) * STAGE, 16, GROUP, SWZ_128B);
-          const uint32_t d = tmem + TM_S + (it & 1) * BN;
+        if (elect_one()) {
+          const uint64_t k0 = make_sdesc(sb + off_kv(a.rb) + st * STAGE, 16, GROUP, SWZ_128B);
+          const uint32_t d = tmem + TM_S + (it & 7) * BN;
 #pragma unroll 1
           for (int blk = 0; blk < 9; ++blk)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_bf16(d, q0 + blk * q_blk + ((kk * 32) >> 4), k0 + ((blk * 1024 + kk * 32) >> 4), idesc_s,
+              umma_bf16(d, q0 + blk * q_blk + ((kk * 32) >> 4), k0 + ((blk * 1024 + kk * 32) >> 4), idesc,
                         (blk > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(&bars[B_SFULL + (it & 1)]);
+          umma_commit(&bars[B_SFULL + (it & 7)]);
           if (i + 1 == w.t1) umma_commit(&bars[B_QFREE]);
         }
-        if (i > w.t0) pv(i - 1, it - 1);
       }
-      if (alive) pv(w.t1 - 1, it - 1);
+      if (!alive) break;
     }
-    if (!alive && lane == 0) {
+    if (!alive && elect_one()) {
       umma_commit(&bars[B_DRAIN]);
       settle_bar(&bars[B_DRAIN], 0);
+    }
+    __syncwarp();
+  } else if (warp == 6) {
+    // ---- O^T += V^T P^T ----
+    const uint32_t sb = smem_u32(sm);
+    const uint32_t idesc = idesc_bf16(128, (uint32_t)a.rb, 1, 0);
+    const uint64_t p0 = make_sdesc(sb + off_p(a.rb), 16, 512, SWZ_64B);
+    int it = 0, sg = 0, st = 0;
+    bool alive = true;
+    for (; more && alive; more = w.next(a), ++sg) {
+      if (sg > 0) alive = wait(&bars[B_OFREE], (sg - 1) & 1);
+      for (int i = w.t0; i < w.t1 && alive; ++i, ++it, st = st + 1 == stages ? 0 : st + 1) {
+        if (!(alive = wait(&bars[B_PFULL + (it & 1)], (it >> 1) & 1))) break;
+        tc_fence_after();
+        const int steps = min(BN / 16, (w.len - i * BN + 15) >> 4);
+        if (elect_one()) {
+          const uint64_t v0 = make_sdesc(sb + off_kv(a.rb) + st * STAGE, 1024, GROUP, SWZ_128B);
+#pragma unroll 1
+          for (int kk = 0; kk < steps; ++kk)
+#pragma unroll
+            for (int mb = 0; mb < 4; ++mb)
+              umma_bf16(tmem + TM_O + mb * 64, v0 + ((kk * 2 * GROUP + mb * 2048) >> 4),
+                        p0 + (((it & 1) * p_bytes(a.rb) + kk * 32) >> 4), idesc, (i > w.t0 || kk > 0) ? 1u : 0u);
+          umma_commit(&bars[B_KVFREE + st]);
+          umma_commit(&bars[B_PVDONE + (it & 1)]);
+        }
+      }
+      if (!alive) break;
+    }
+    if (!alive && elect_one()) {
+      umma_commit(&bars[B_DRAIN + 1]);
+      settle_bar(&bars[B_DRAIN + 1], 0);
     }
     __syncwarp();
   } else {
@@ -355,74 +414,66 @@ kda_mla_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         }
       }
       const int prefix = w.len - a.n_tokens;   // rows every token sees (may be negative)
+      // No warp leaves the loop on its own: after a timeout every wait fails at once and the
+      // tiles run out, so that the four warps always meet at the same barriers.
       for (int i = w.t0; i < w.t1; ++i, ++it) {
-        // (no warp leaves on its own: a timeout is carried to the vote below, so that the four
-        // warps always meet at the same barriers)
-        alive = wait(&bars[B_SFULL + (it & 1)], (it >> 1) & 1);
+        const uint32_t half = (it >> 1) & 1;
+        alive = wait(&bars[B_SFULL + (it & 7)], (it >> 3) & 1) && alive;
         tc_fence_after();
-        float s[32];
+        float s[16];
         bool move = false;
         float f[2] = {1.f, 1.f};
         if (busy) {
-          uint32_t* u = reinterpret_cast<uint32_t*>(s);
-          tmem_ld16x256b_x4(tmem + TM_S + (it & 1) * BN + lane_base, *reinterpret_cast<uint32_t(*)[16]>(u));
-          tmem_ld16x256b_x4(tmem + TM_S + (it & 1) * BN + 32 + lane_base, *reinterpret_cast<uint32_t(*)[16]>(u + 16));
+          tmem_ld16x256b_x4(tmem + TM_S + (it & 7) * BN + lane_base, *reinterpret_cast<uint32_t(*)[16]>(&s));
           tmem_ld_wait();
           if ((i + 1) * BN > prefix) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < 16; ++e) {
               const int d = i * BN + 8 * (e >> 2) + 2 * (lane & 3) + (e & 1) - prefix;   // the row among the newest
               const bool seen = d < 0 || (d < a.n_tokens && ((bits[(e >> 1) & 1] >> d) & 1u));
               if (!seen) s[e] = -INFINITY;
             }
           }
-          float mt[2] = {s[0], s[2]};
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            mt[0] = fmaxf(mt[0], fmaxf(s[e], s[e + 1]));
-            mt[1] = fmaxf(mt[1], fmaxf(s[e + 2], s[e + 3]));
-          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 1));
-            mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 2));
+            float mt = fmaxf(fmaxf(fmaxf(s[2 * h], s[2 * h + 1]), fmaxf(s[2 * h + 4], s[2 * h + 5])),
+                             fmaxf(fmaxf(s[2 * h + 8], s[2 * h + 9]), fmaxf(s[2 * h + 12], s[2 * h + 13])));
+            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
             if (i == w.t0) {
-              m[h] = mt[h];
-            } else if (mt[h] > m[h] && (mt[h] - m[h]) * sc > RESCALE_LOG2) {
-              f[h] = exp2_fast((m[h] - mt[h]) * sc);
+              m[h] = mt;
+            } else if (mt > m[h] && (mt - m[h]) * sc > RESCALE_LOG2) {
+              f[h] = exp2_fast((m[h] - mt) * sc);
               l[h] *= f[h];
-              m[h] = mt[h];
+              m[h] = mt;
               move = true;
             }
           }
         }
         const bool rescale = i > w.t0 && named_bar_or(1, 128, move);
-        uint32_t p[16];
+        uint32_t p[8];
         if (busy) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float ms = m[h] == -INFINITY ? 0.f : m[h] * sc;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
+            for (int e = 0; e < 16; e += 4) {
               const float e0 = exp2_fast(fmaf(s[e + 2 * h], sc, -ms)), e1 = exp2_fast(fmaf(s[e + 2 * h + 1], sc, -ms));
               l[h] += e0 + e1;
               p[(e >> 1) + h] = pack2(e0, e1);
             }
           }
         }
-        if (i > w.t0) {   // P and the accumulators are the tile before's until its products are done
-          alive = wait(&bars[B_PVDONE], (it - 1) & 1) && alive;
+        // the P buffer is free once the products of two tiles before are done
+        if (it >= 2) alive = wait(&bars[B_PVDONE + (it & 1)], half ^ 1u) && alive;
+        if (rescale) {   // and the accumulators with those of the tile before
+          if (busy && (lane & 3) == 0) {
+            s_fac[ra] = f[0];
+            s_fac[ra + 8] = f[1];
+          }
+          alive = wait(&bars[B_PVDONE + ((it - 1) & 1)], ((it - 1) >> 1) & 1) && alive;
           tc_fence_after();
-        }
-        if (rescale && busy && (lane & 3) == 0) {
-          s_fac[ra] = f[0];
-          s_fac[ra + 8] = f[1];
-        }
-        if (named_bar_or(2, 128, !alive)) {
-          alive = false;
-          break;
-        }
-        if (rescale) {
+          named_bar_sync(1, 128);
           for (int mb = 0; mb < 4; ++mb)
             for (int c = 0; c < a.rb; c += 16) {
               float v[16];
@@ -438,16 +489,16 @@ kda_mla_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         if (busy) {
           const int mi = lane >> 3;
 #pragma unroll
-          for (int k = 0; k < 8; k += 2) {
+          for (int k = 0; k < 4; k += 2) {
             const uint32_t row = (uint32_t)(16 * warp + (mi & 1) * 8 + (lane & 7)), col = 8u * (k + (mi >> 1));
-            stmatrix_x4(p_base + swz128(row * 128u + col * 2u), p[2 * k], p[2 * k + 1], p[2 * k + 2], p[2 * k + 3]);
+            stmatrix_x4(p_base + (it & 1) * p_bytes(a.rb) + swz64(row * 64u + col * 2u), p[2 * k], p[2 * k + 1],
+                        p[2 * k + 2], p[2 * k + 3]);
           }
           fence_proxy_async_smem();
         }
         tc_fence_before();
-        mbar_arrive(&bars[B_PFULL]);
+        mbar_arrive(&bars[B_PFULL + (it & 1)]);
       }
-      if (!alive) break;
       // output: every row's maximum and sum, then the accumulators
       const bool whole = w.t0 == 0 && w.t1 == w.tiles;
       const int slot = 2 * (int)blockIdx.x + (w.t0 == 0 ? 1 : 0);
@@ -472,7 +523,7 @@ kda_mla_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
           }
         }
       }
-      alive = wait(&bars[B_PVDONE], (it - 1) & 1);
+      alive = wait(&bars[B_PVDONE + ((it - 1) & 1)], ((it - 1) >> 1) & 1) && alive;
       tc_fence_after();
       alive = !named_bar_or(2, 128, !alive);
       if (!alive) break;
@@ -511,15 +562,21 @@ kda_mla_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
 }
 
 // Joins the items that a run's border cuts. With no more items than borders a block takes an
-// item, else a border (and the item that it cuts, if it is the first to cut it); blockIdx.y
-// takes rows, four groups of 128 threads every fourth part.
-constexpr int JOIN_THREADS = 512;
+// item, else a border (and the item that it cuts, if it is the first to cut it). A row is one
+// warp's (ALONE: most items have two or three parts) or one block's (few items of many parts:
+// the warps take every eighth part each). Which part holds what follows from the lengths alone,
+// so it is worked out while the main kernel's last CTAs still run; 19 to 38 MB of sums, mostly
+// from L2.
+constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_THREADS = 32 * JOIN_WARPS;
 
+template <bool ALONE>
 __global__ void __launch_bounds__(JOIN_THREADS)
-kda_mla_decode_join_kernel(const Args a, int by_item, int rows_per_block) {
-  __shared__ int64_t s_sums[JOIN_THREADS / 32], s_found[2];
-  __shared__ float4 s_acc[3][128];
-  const int tid = threadIdx.x;
+kda_mla_decode_join_kernel(const Args a, int by_item) {
+  __shared__ int64_t s_sums[JOIN_WARPS], s_found[2], s_mine[JOIN_WARPS];
+  __shared__ float4 s_acc[ALONE ? 1 : JOIN_WARPS][LATENT / 4];
+  __shared__ float s_l[JOIN_WARPS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int workers, n, g, tiles;
   int64_t begin, end, first_at, total, f;
   if (by_item) {
@@ -537,14 +594,13 @@ kda_mla_decode_join_kernel(const Args a, int by_item, int rows_per_block) {
       mine += __shfl_xor_sync(0xffffffffu, mine, off);
       all += __shfl_xor_sync(0xffffffffu, all, off);
     }
-    __shared__ int64_t s_mine[JOIN_THREADS / 32];
-    if ((tid & 31) == 0) {
-      s_sums[tid >> 5] = all;
-      s_mine[tid >> 5] = mine;
+    if (lane == 0) {
+      s_sums[warp] = all;
+      s_mine[warp] = mine;
     }
     __syncthreads();
     total = f = 0;
-    for (int k = 0; k < JOIN_THREADS / 32; ++k) {
+    for (int k = 0; k < JOIN_WARPS; ++k) {
       total += s_sums[k];
       f += s_mine[k];
     }
@@ -552,9 +608,15 @@ kda_mla_decode_join_kernel(const Args a, int by_item, int rows_per_block) {
     tiles = seq_tiles(a, n);
     f = f * a.groups + (int64_t)g * tiles;
     workers = worker_count(a, total);
-    if (tiles == 0) return;
   } else {
     total = locate<JOIN_THREADS>(a, s_sums, s_found, blockIdx.x + 1, workers, begin, end, n, first_at);
+  }
+  // Every block waits, also one with nothing to do: what follows in the stream counts on the
+  // main kernel's end too.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (by_item) {
+    if (tiles == 0) return;
+  } else {
     if (begin >= end) return;
     tiles = seq_tiles(a, n);
     g = (int)((begin - first_at) / tiles);
@@ -563,50 +625,64 @@ kda_mla_decode_join_kernel(const Args a, int by_item, int rows_per_block) {
   }
   const int b0 = (int)(((f + 1) * workers - 1) / total), b1 = (int)(((f + tiles) * workers - 1) / total);
   if (b0 == b1 || (!by_item && b0 != (int)blockIdx.x)) return;
-  const int grp = tid >> 7, c = tid & 127;
-  const float* ml0 = a.part + (int64_t)2 * a.grid * a.rb * LATENT;
-  const int r_end = min(a.rb, a.rows - g * a.rb);
-  for (int r = blockIdx.y * rows_per_block; r < min(r_end, (int)(blockIdx.y + 1) * rows_per_block); ++r) {
-    float m = -INFINITY;
-    for (int b = b0; b <= b1; ++b) m = fmaxf(m, ml0[((int64_t)(2 * b + (b == b0)) * a.rb + r) * 2]);
-    const float ms = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int b = b0 + grp; b <= b1; b += 4) {
-      const int64_t row = (int64_t)(2 * b + (b == b0)) * a.rb + r;
-      const float w = exp2_fast(ml0[row * 2] - ms);
-      const float4 v = reinterpret_cast<const float4*>(a.part + row * LATENT)[c];
-      l = fmaf(w, ml0[row * 2 + 1], l);
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z);
-      acc.w = fmaf(w, v.w, acc.w);
-    }
-    __shared__ float s_l[4];
-    if (grp > 0) s_acc[grp - 1][c] = acc;
-    if (c == 0) s_l[grp] = l;
-    __syncthreads();
-    if (grp == 0) {
+  const int r = ALONE ? (int)blockIdx.y * JOIN_WARPS + warp : (int)blockIdx.y;
+  if (r >= min(a.rb, a.rows - g * a.rb)) return;   // (not ALONE: the same for the whole block)
+
+  // row of the part that worker b left: its second slot if the item begins in it, else its first
+  const float* ml = a.part + (int64_t)2 * a.grid * a.rb * LATENT;
+  auto row_of = [&](int b) { return (int64_t)(2 * b + (b == b0)) * a.rb + r; };
+  float m = -INFINITY;
+  for (int b = b0 + lane; b <= b1; b += 32) m = fmaxf(m, ml[row_of(b) * 2]);
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const float4 v = s_acc[k][c];
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
-      }
-      const float lt = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
-      const int64_t row = (int64_t)n * a.rows + g * a.rb + r;
-      const float inv = lt == 0.f ? 0.f : 1.f / lt;
-      uint2 out = make_uint2(0, 0);
-      if (lt != 0.f) out = make_uint2(pack2(acc.x * inv, acc.y * inv), pack2(acc.z * inv, acc.w * inv));
-      reinterpret_cast<uint2*>(a.o + row * LATENT)[c] = out;
-      if (a.lse && c == 0)
-        a.lse[row] = lt == 0.f ? -INFINITY : ms * 0.6931471805599453f + logf(lt);
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  const float ms = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int STEP = ALONE ? 1 : JOIN_WARPS;
+#pragma unroll 2
+  for (int b = b0 + (ALONE ? 0 : warp); b <= b1; b += STEP) {
+    const int64_t row = row_of(b);
+    const float w = exp2_fast(ml[row * 2] - ms);
+    const float4* src = reinterpret_cast<const float4*>(a.part + row * LATENT);
+    l = fmaf(w, ml[row * 2 + 1], l);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 v = src[32 * k + lane];
+      acc[k].x = fmaf(w, v.x, acc[k].x);
+      acc[k].y = fmaf(w, v.y, acc[k].y);
+      acc[k].z = fmaf(w, v.z, acc[k].z);
+      acc[k].w = fmaf(w, v.w, acc[k].w);
     }
-    __syncthreads();
   }
+  const int64_t row = (int64_t)n * a.rows + g * a.rb + r;
+  uint2* od = reinterpret_cast<uint2*>(a.o + row * LATENT);
+  if constexpr (!ALONE) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s_acc[warp][32 * k + lane] = acc[k];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (tid >= LATENT / 4) return;
+    l = 0.f;
+    acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < JOIN_WARPS; ++k) {
+      const float4 v = s_acc[k][tid];
+      l += s_l[k];
+      acc[0].x += v.x;
+      acc[0].y += v.y;
+      acc[0].z += v.z;
+      acc[0].w += v.w;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int k = 0; k < (ALONE ? 4 : 1); ++k)
+    od[ALONE ? 32 * k + lane : tid] =
+        l == 0.f ? make_uint2(0, 0)
+                 : make_uint2(pack2(acc[k].x * inv, acc[k].y * inv), pack2(acc[k].z * inv, acc[k].w * inv));
+  if (a.lse && (ALONE ? lane : tid) == 0) a.lse[row] = l == 0.f ? -INFINITY : ms * 0.6931471805599453f + logf(l);
 }
 
 }  // namespace dec
