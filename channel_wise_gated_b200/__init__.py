@@ -42,6 +42,9 @@ def _stream_ptr(device) -> int:
 
 
 def _need(t: torch.Tensor, name: str, dtype=None, shape=None, device=None):
+    if (shape is not None and device is not None and isinstance(t, torch.Tensor) and t.is_cuda
+            and t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        return   # (all is well in one pass; what is not is named below)
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -58,6 +61,20 @@ def _need(t: torch.Tensor, name: str, dtype=None, shape=None, device=None):
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
+
+
+def _launch(fn, where, dev, *args):
+    """Call an entry point on dev's current stream, with dev the current device. (A device guard
+    and a Stream object cost 3.6 us of a call's host time: the guard is taken only where it is
+    needed, the stream's handle read as it is.)"""
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st:
+        _native.check(st, where)
 
 
 def _prefill_args(q, k, v, gate, gate_shape_tail, beta, h0, cu_seqlens, o, hT,
@@ -362,11 +379,9 @@ def decode_tree(q, k, v, log_alpha, beta, state, tree=None, o=None):
         o = torch.empty_like(q)
     else:
         _need(o, "o", q.dtype, (N, t, H, D), dev)
-    with torch.cuda.device(dev):
-        st = lib.kda_decode_tree(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta),
-                                 _ptr(state), _ptr(tree), _ptr(o), N, t, H, _DT[q.dtype],
-                                 _DT[log_alpha.dtype], _stream_ptr(dev))
-    _native.check(st, "kda_decode_tree")
+    _launch(lib.kda_decode_tree, "kda_decode_tree", dev, _ptr(q), _ptr(k), _ptr(v),
+            _ptr(log_alpha), _ptr(beta), _ptr(state), _ptr(tree), _ptr(o), N, t, H, _DT[q.dtype],
+            _DT[log_alpha.dtype])
     return o
 
 
@@ -381,8 +396,10 @@ def _need_rows(t, name, dtype, shape, device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.is_contiguous() and all(n % 8 == 0 for n in t.shape[1:]):
+        return
     if t.stride(-1) != 1 or any(s % 8 for n, s in zip(t.shape, t.stride()[:-1]) if n > 1):
         raise ValueError(f"{name} must have a dense last dimension and strides in multiples of 8")
 
@@ -431,12 +448,9 @@ def mla_append(x, norm_w, cache, page_table, cache_lens, cu_seqlens=None, latent
         _need(latent, "latent", torch.bfloat16, (T, MLA_LATENT), dev)
     elif output_latent:
         latent = torch.empty((T, MLA_LATENT), dtype=torch.bfloat16, device=dev)
-    with torch.cuda.device(dev):
-        st = lib.kda_mla_append(_ptr(x), _row_stride(x, 0, MLA_WIDTH), _ptr(norm_w), float(eps),
-                                _ptr(cache), n_pages, page_size, _ptr(page_table), max_pages,
-                                _ptr(cache_lens), _ptr(cu_seqlens), N, T, _ptr(latent),
-                                _stream_ptr(dev))
-    _native.check(st, "kda_mla_append")
+    _launch(lib.kda_mla_append, "kda_mla_append", dev, _ptr(x), _row_stride(x, 0, MLA_WIDTH),
+            _ptr(norm_w), float(eps), _ptr(cache), n_pages, page_size, _ptr(page_table), max_pages,
+            _ptr(cache_lens), _ptr(cu_seqlens), N, T, _ptr(latent))
     return latent
 
 
@@ -475,7 +489,7 @@ def mla_prefill(q, k, k_shared, v, cu_seqlens=None, cu_seqlens_k=None, scale=Non
     elif cu_seqlens_k is not None:
         raise ValueError("cu_seqlens_k needs cu_seqlens")
     if o is None:
-        o = torch.empty((Tq, H, D), dtype=torch.bfloat16, device=dev)
+        o = q.new_empty((Tq, H, D))
     else:
         _need(o, "o", torch.bfloat16, (Tq, H, D), dev)
     if lse is not None:
@@ -489,13 +503,21 @@ def mla_prefill(q, k, k_shared, v, cu_seqlens=None, cu_seqlens_k=None, scale=Non
         th = _row_stride(t, 1, width)
         return _ptr(t), _row_stride(t, 0, H * th), th
 
-    with torch.cuda.device(dev):
-        st = lib.kda_mla_prefill(*strides(q, D + MLA_SHARED), *strides(k, D), _ptr(k_shared),
-                                 _row_stride(k_shared, 0, MLA_SHARED), *strides(v, D),
-                                 _ptr(cu_seqlens), _ptr(cu_seqlens_k), N, Tq, Tk, H, float(scale),
-                                 int(causal), _ptr(o), _ptr(lse), _stream_ptr(dev))
-    _native.check(st, "kda_mla_prefill")
+    _launch(lib.kda_mla_prefill, "kda_mla_prefill", dev, *strides(q, D + MLA_SHARED), *strides(k, D),
+            _ptr(k_shared), _row_stride(k_shared, 0, MLA_SHARED), *strides(v, D), _ptr(cu_seqlens),
+            _ptr(cu_seqlens_k), N, Tq, Tk, H, float(scale), int(causal), _ptr(o), _ptr(lse))
     return o, lse
+
+
+def mla_decode_workspace_size(n_tokens: int, n_heads: int, device=None) -> int:
+    """Bytes of workspace that mla_decode takes on the device (default: the current one), for any
+    number and length of sequences."""
+    lib = _native.load()
+    dev = None if device is None else torch.device(device).index
+    if dev is None or dev == torch.cuda.current_device():
+        return lib.kda_mla_decode_workspace_size(int(n_tokens), int(n_heads))
+    with torch.cuda.device(dev):
+        return lib.kda_mla_decode_workspace_size(int(n_tokens), int(n_heads))
 
 
 def mla_decode(q, cache, page_table, cache_lens, tree=None, scale=None, o=None, lse=None,
@@ -506,7 +528,7 @@ def mla_decode(q, cache, page_table, cache_lens, tree=None, scale=None, o=None, 
     values); cache: [n_pages, page_size, 576] bf16, page_size a multiple of 8; page_table: [N,
     max_pages] int32; cache_lens: [N] int32, lengths with the t new tokens, which mla_append has
     written; tree: [N, t] int32 ancestor bits as decode_tree, or None (a chain). scale:
-    1 / sqrt(192) by default. workspace: uint8 of kda_mla_decode_workspace_size bytes, allocated
+    1 / sqrt(192) by default. workspace: uint8 of mla_decode_workspace_size bytes, allocated
     here if None; calls that may overlap need one each. Returns (o, lse): o [N, t, H, 512] bf16
     in the latent space, lse [N, t, H] fp32 with output_lse (or into lse), else None.
     """
@@ -524,7 +546,7 @@ def mla_decode(q, cache, page_table, cache_lens, tree=None, scale=None, o=None, 
     if tree is not None:
         _need(tree, "tree", torch.int32, (N, t), dev)
     if o is None:
-        o = torch.empty((N, t, H, MLA_LATENT), dtype=torch.bfloat16, device=dev)
+        o = q.new_empty((N, t, H, MLA_LATENT))
     else:
         _need(o, "o", torch.bfloat16, (N, t, H, MLA_LATENT), dev)
     if lse is not None:
@@ -533,17 +555,13 @@ def mla_decode(q, cache, page_table, cache_lens, tree=None, scale=None, o=None, 
         lse = torch.empty((N, t, H), dtype=torch.float32, device=dev)
     if scale is None:
         scale = (D + MLA_SHARED) ** -0.5
-    with torch.cuda.device(dev):
-        if workspace is None:
-            workspace = torch.empty(lib.kda_mla_decode_workspace_size(t, H), dtype=torch.uint8,
-                                    device=dev)
-        else:
-            _need(workspace, "workspace", torch.uint8, None, dev)
-        st = lib.kda_mla_decode(_ptr(q), _ptr(cache), n_pages, page_size, _ptr(page_table),
-                                max_pages, _ptr(cache_lens), _ptr(tree), N, t, H, float(scale),
-                                _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel(),
-                                _stream_ptr(dev))
-    _native.check(st, "kda_mla_decode")
+    if workspace is None:
+        workspace = torch.empty(mla_decode_workspace_size(t, H, dev), dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", torch.uint8, None, dev)
+    _launch(lib.kda_mla_decode, "kda_mla_decode", dev, _ptr(q), _ptr(cache), n_pages, page_size,
+            _ptr(page_table), max_pages, _ptr(cache_lens), _ptr(tree), N, t, H, float(scale),
+            _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel())
     return o, lse
 
 

@@ -869,7 +869,6 @@ int kda_mla_decode(const void* q, const void* cache, int64_t n_pages, int32_t pa
   a.rows = n_tokens * n_heads;
   mla_decode_groups(a.rows, a.groups, a.rb);
   if (workspace_bytes < mla_decode_workspace(sms, a.rb)) return KDA_ERR_SCRATCH;
-  a.cache = cache;
   a.page_table = page_table;
   a.cache_lens = cache_lens;
   a.tree = tree;
@@ -901,17 +900,21 @@ int kda_mla_decode(const void* q, const void* cache, int64_t n_pages, int32_t pa
     // (the join's launch overlaps the end of the main kernel, which it waits for itself)
     const int64_t items = (int64_t)n_seqs * a.groups;
     const int by_item = items <= a.grid - 1;
-    const bool alone = items * 8 > a.grid;
+    const bool alone = items * 16 > a.grid;   // (up to 16 parts an item: a warp takes a row)
     cudaLaunchAttribute early;
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)(by_item ? items : a.grid - 1),
-                     (unsigned)(alone ? (a.rb + JOIN_WARPS - 1) / JOIN_WARPS : a.rb));
+                     (unsigned)(alone ? (a.rb + JOIN_WARPS - 1) / JOIN_WARPS : 4 * a.rb));
     c.blockDim = dim3(JOIN_THREADS);
     c.stream = stream;
     c.attrs = &early;
     c.numAttrs = 1;
+    // (the same split of L1 as the main kernel's: an SM that changes it drains first)
+    if (cudaFuncSetAttribute(alone ? (const void*)kda_mla_decode_join_kernel<true> : (const void*)kda_mla_decode_join_kernel<false>,
+                             cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+      return KDA_ERR_CUDA;
     const cudaError_t e = alone ? cudaLaunchKernelEx(&c, kda_mla_decode_join_kernel<true>, a, by_item)
                                 : cudaLaunchKernelEx(&c, kda_mla_decode_join_kernel<false>, a, by_item);
     if (e != cudaSuccess || launch_status() != KDA_OK) return KDA_ERR_CUDA;

@@ -39,8 +39,11 @@ constexpr int THREADS = 224;
 constexpr uint32_t GROUP = 8 * WIDTH * 2;               // 8 cached rows: nine 1 KiB swizzle atoms
 constexpr uint32_t STAGE = BN / 8 * GROUP;              // 36,864 bytes
 constexpr int MAX_STAGES = 5;
-constexpr int FETCH = 4;                                // tiles from a piece's L2 prefetch to its copy
-constexpr int MIN_TILES = 2;                            // a CTA's run is at least this long
+constexpr int LOOK = 4;                                 // tiles from reading a page's number to its copy
+// A CTA's run is at least this long: one sequence of 640 / 5,000 / 9,000 rows took 11.2 / 15.0 /
+// 20.4 us with 2 (more parts to join, and no idle SM for the join to start on), 12.1 / 14.8 / 17.6
+// with 3, 12.9 / 15.3 / 16.7 with 4.
+constexpr int MIN_TILES = 3;
 enum { B_KVFULL = 0, B_KVFREE = MAX_STAGES, B_SFULL = 2 * MAX_STAGES, B_PFULL = B_SFULL + 8, B_PVDONE = B_PFULL + 2,
        B_QFULL = B_PVDONE + 2, B_QFREE, B_OFREE, B_DRAIN, N_BARS = B_DRAIN + 2 };
 constexpr uint32_t TM_O = 0, TM_S = 256;                // four accumulators 64 columns apart; eight S
@@ -62,7 +65,6 @@ static_assert(smem_bytes(16) <= SMEM_MOST && smem_bytes(32) <= SMEM_MOST && smem
               "shared memory of one CTA");
 
 struct Args {
-  const void* cache;
   const int32_t* page_table;
   const int32_t* cache_lens;
   const int32_t* tree;
@@ -241,15 +243,14 @@ kda_mla_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
 
   if (warp == 4) {
     // ---- copies: lane c brings the c-th piece of page_rows rows of a tile ----
-    // The stages that a tile's products do not hold cover about 110 KiB of copies in flight per
-    // SM, too little for HBM's latency under load (2.7 us a tile, 4.0 TB/s): so every piece is
-    // brought into L2 FETCH tiles ahead of its copy, along with reading its page's number.
+    // The page's number is read LOOK tiles ahead of the copy, off its path. (Bringing the piece
+    // into L2 along with it gained nothing: 152 against 148 us for 128 sequences.)
     const int pieces = BN / a.page_rows;
     Walk wa = w;
     int ia = w.t0;
     bool a_left = more;
     // the cursor's piece of this lane: its first row over 8, or -1; then a tile further
-    auto look = [&](bool fetch) {
+    auto look = [&]() {
       int row8 = -1;
       if (a_left) {
         const int pos = ia * BN + lane * a.page_rows;
@@ -261,11 +262,6 @@ kda_mla_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             page = 0;
           }
           row8 = (int)(((int64_t)page * a.page_size + (pos - pi * a.page_size)) >> 3);
-          if (fetch)
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                             reinterpret_cast<const unsigned char*>(a.cache) + (int64_t)row8 * GROUP),
-                         "r"((uint32_t)a.page_rows * (WIDTH * 2))
-                         : "memory");
         }
         if (++ia == wa.t1) {
           a_left = wa.next(a);
@@ -274,17 +270,17 @@ kda_mla_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
       }
       return row8;
     };
-    int queue[FETCH];
+    int queue[LOOK];
 #pragma unroll
-    for (int k = 0; k < FETCH; ++k) queue[k] = look(k >= 2);
+    for (int k = 0; k < LOOK; ++k) queue[k] = look();
     int it = 0, sg = 0, st = 0, round = 0;   // tile, item, stage and its use
     bool alive = true;
     for (; more && alive; more = w.next(a), ++sg) {
       for (int i = w.t0; i < w.t1 && alive; ++i, ++it, st = st + 1 == stages ? 0 : st + 1, round += st == 0) {
         const int row8 = queue[0];
 #pragma unroll
-        for (int k = 1; k < FETCH; ++k) queue[k - 1] = queue[k];
-        queue[FETCH - 1] = look(true);
+        for (int k = 1; k < LOOK; ++k) queue[k - 1] = queue[k];
+        queue[LOOK - 1] = look();
         const int count = __popc(__ballot_sync(0xffffffffu, row8 >= 0));
         uint64_t* full = &bars[B_KVFULL + st];
         if (round > 0) alive = wait(&bars[B_KVFREE + st], (round - 1) & 1);
@@ -563,8 +559,10 @@ kda_mla_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
 
 // Joins the items that a run's border cuts. With no more items than borders a block takes an
 // item, else a border (and the item that it cuts, if it is the first to cut it). A row is one
-// warp's (ALONE: most items have two or three parts) or one block's (few items of many parts:
-// the warps take every eighth part each). Which part holds what follows from the lengths alone,
+// warp's (ALONE: most items have two or three parts) or four blocks' (few items of many parts: a
+// block takes 128 of the latents, its warps every eighth part each). Its shared memory is small
+// enough for a block to wait beside a CTA of the main kernel of up to 48 rows: with room for
+// that, 5,000 rows of one sequence take 15 us, without it 20. Which part holds what follows from the lengths alone,
 // so it is worked out while the main kernel's last CTAs still run; 19 to 38 MB of sums, mostly
 // from L2.
 constexpr int JOIN_WARPS = 8;
@@ -574,7 +572,8 @@ template <bool ALONE>
 __global__ void __launch_bounds__(JOIN_THREADS)
 kda_mla_decode_join_kernel(const Args a, int by_item) {
   __shared__ int64_t s_sums[JOIN_WARPS], s_found[2], s_mine[JOIN_WARPS];
-  __shared__ float4 s_acc[ALONE ? 1 : JOIN_WARPS][LATENT / 4];
+  constexpr int SPAN = ALONE ? 4 : 1;   // 16-byte pieces of a row per lane
+  __shared__ float4 s_acc[ALONE ? 1 : JOIN_WARPS / 2][32];
   __shared__ float s_l[JOIN_WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int workers, n, g, tiles;
@@ -625,7 +624,8 @@ kda_mla_decode_join_kernel(const Args a, int by_item) {
   }
   const int b0 = (int)(((f + 1) * workers - 1) / total), b1 = (int)(((f + tiles) * workers - 1) / total);
   if (b0 == b1 || (!by_item && b0 != (int)blockIdx.x)) return;
-  const int r = ALONE ? (int)blockIdx.y * JOIN_WARPS + warp : (int)blockIdx.y;
+  const int r = ALONE ? (int)blockIdx.y * JOIN_WARPS + warp : (int)blockIdx.y >> 2;
+  const int c0 = ALONE ? 0 : 32 * ((int)blockIdx.y & 3);   // first piece
   if (r >= min(a.rb, a.rows - g * a.rb)) return;   // (not ALONE: the same for the whole block)
 
   // row of the part that worker b left: its second slot if the item begins in it, else its first
@@ -637,19 +637,19 @@ kda_mla_decode_join_kernel(const Args a, int by_item) {
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   const float ms = m == -INFINITY ? 0.f : m;
   float l = 0.f;
-  float4 acc[4];
+  float4 acc[SPAN];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < SPAN; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int STEP = ALONE ? 1 : JOIN_WARPS;
-#pragma unroll 2
+#pragma unroll (ALONE ? 3 : 8)
   for (int b = b0 + (ALONE ? 0 : warp); b <= b1; b += STEP) {
     const int64_t row = row_of(b);
     const float w = exp2_fast(ml[row * 2] - ms);
     const float4* src = reinterpret_cast<const float4*>(a.part + row * LATENT);
     l = fmaf(w, ml[row * 2 + 1], l);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float4 v = src[32 * k + lane];
+    for (int k = 0; k < SPAN; ++k) {
+      const float4 v = src[c0 + 32 * k + lane];
       acc[k].x = fmaf(w, v.x, acc[k].x);
       acc[k].y = fmaf(w, v.y, acc[k].y);
       acc[k].z = fmaf(w, v.z, acc[k].z);
@@ -659,30 +659,33 @@ kda_mla_decode_join_kernel(const Args a, int by_item) {
   const int64_t row = (int64_t)n * a.rows + g * a.rb + r;
   uint2* od = reinterpret_cast<uint2*>(a.o + row * LATENT);
   if constexpr (!ALONE) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) s_acc[warp][32 * k + lane] = acc[k];
     if (lane == 0) s_l[warp] = l;
-    __syncthreads();
-    if (tid >= LATENT / 4) return;
-    l = 0.f;
-    acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < JOIN_WARPS; ++k) {
-      const float4 v = s_acc[k][tid];
-      l += s_l[k];
-      acc[0].x += v.x;
-      acc[0].y += v.y;
-      acc[0].z += v.z;
-      acc[0].w += v.w;
+    for (int half = JOIN_WARPS / 2; half > 0; half >>= 1) {   // the upper half's sums onto the lower's
+      if (warp >= half && warp < 2 * half) s_acc[warp - half][lane] = acc[0];
+      __syncthreads();
+      if (warp < half) {
+        const float4 v = s_acc[warp][lane];
+        acc[0].x += v.x;
+        acc[0].y += v.y;
+        acc[0].z += v.z;
+        acc[0].w += v.w;
+      }
+      __syncthreads();
     }
+    if (warp != 0) return;
+    l = 0.f;
+#pragma unroll
+    for (int k = 0; k < JOIN_WARPS; ++k) l += s_l[k];
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-  for (int k = 0; k < (ALONE ? 4 : 1); ++k)
-    od[ALONE ? 32 * k + lane : tid] =
+  for (int k = 0; k < SPAN; ++k)
+    od[c0 + 32 * k + lane] =
         l == 0.f ? make_uint2(0, 0)
                  : make_uint2(pack2(acc[k].x * inv, acc[k].y * inv), pack2(acc[k].z * inv, acc[k].w * inv));
-  if (a.lse && (ALONE ? lane : tid) == 0) a.lse[row] = l == 0.f ? -INFINITY : ms * 0.6931471805599453f + logf(l);
+  if (a.lse && c0 == 0 && lane == 0)
+    a.lse[row] = l == 0.f ? -INFINITY : ms * 0.6931471805599453f + logf(l);
 }
 
 }  // namespace dec
