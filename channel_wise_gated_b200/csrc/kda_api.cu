@@ -379,13 +379,13 @@ bool encode_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dim
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A [tokens, heads, width] tensor with a dense last dimension, in boxes of 128 tokens of one
+// A [tokens, heads, width] tensor with a dense last dimension, in boxes of box_t tokens of one
 // head and 64 columns.
 bool encode_heads(CUtensorMap* m, const void* base, uint64_t width, int32_t heads, int64_t tokens,
-                  int64_t stride_t, int64_t stride_h) {
+                  int64_t stride_t, int64_t stride_h, uint32_t box_t) {
   const uint64_t dims[3] = {width, (uint64_t)heads, (uint64_t)tokens};
   const uint64_t strides[2] = {(uint64_t)stride_h * 2, (uint64_t)stride_t * 2};
-  const uint32_t box[3] = {64, 1, 128};
+  const uint32_t box[3] = {64, 1, box_t};
   return encode_bf16(m, base, 3, dims, strides, box);
 }
 
@@ -812,13 +812,13 @@ int kda_mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const
   memset(&mk, 0, sizeof(mk));   // (without keys no kernel touches the maps)
   memset(&ms, 0, sizeof(ms));
   memset(&mv, 0, sizeof(mv));
-  bool ok = encode_heads(&mq, q, DQ, n_heads, tq_total, q_stride_t, q_stride_h);
+  bool ok = encode_heads(&mq, q, DQ, n_heads, tq_total, q_stride_t, q_stride_h, 128);
   if (tk_total > 0) {
     const uint64_t dims[2] = {(uint64_t)kda::mla::SHARED_K, (uint64_t)tk_total};
     const uint64_t strides[1] = {(uint64_t)ks_stride_t * 2};
     const uint32_t box[2] = {64, 128};
-    ok = ok && encode_heads(&mk, k, kda::D, n_heads, tk_total, k_stride_t, k_stride_h) &&
-         encode_heads(&mv, v, kda::D, n_heads, tk_total, v_stride_t, v_stride_h) &&
+    ok = ok && encode_heads(&mk, k, kda::D, n_heads, tk_total, k_stride_t, k_stride_h, 128) &&
+         encode_heads(&mv, v, kda::D, n_heads, tk_total, v_stride_t, v_stride_h, 64) &&
          encode_bf16(&ms, k_shared, 2, dims, strides, box);
   }
   if (!ok || cudaFuncSetAttribute(kda_mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -90,15 +90,20 @@ namespace pf {
 constexpr int BM = 128;             // queries per tile
 constexpr int PAIR = 2 * BM;        // queries per CTA
 constexpr int BN = 128;             // keys per tile
-constexpr int THREADS = 384;        // (warps 10 and 11 idle: registers are split by groups of four)
-constexpr uint32_t BLK = 128 * 128; // a 128-row block of 64 bf16 columns, 16 KiB
-constexpr uint32_t Q_BYTES = 3 * BLK, K_BYTES = 3 * BLK, V_BYTES = 2 * BLK;
-constexpr uint32_t OFF_Q = 0, OFF_K = 2 * Q_BYTES, OFF_V = OFF_K + 2 * K_BYTES;
-constexpr uint32_t OFF_BAR = OFF_V + V_BYTES;
+constexpr int THREADS = 384;        // (warp 11 idle: registers are split by groups of four)
+constexpr uint32_t BLK = 128 * 128; // 16 KiB: a 128-row block of 64 bf16 columns
+constexpr uint32_t Q_BYTES = 3 * BLK;
+constexpr int SLOTS = 8;            // keys and values pass through a ring of 16 KiB slots: a tile's
+constexpr int PER_TILE = 5;         // keys in three (64 columns each), its values in two (64 rows each)
+constexpr uint32_t OFF_Q = 0, OFF_RING = 2 * Q_BYTES;
+constexpr uint32_t OFF_BAR = OFF_RING + SLOTS * BLK;
 constexpr uint32_t SMEM_BYTES = OFF_BAR + 256 + 1024;   // (1 KiB to align the base)
 static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
 
-enum { B_QFULL = 0, B_KFULL = 2, B_KFREE = 4, B_VFULL = 6, B_VFREE, B_SFULL = 8, B_PFULL = 10, B_OFULL = 12, B_DRAIN = 14, N_BARS };
+// (P's barriers: two halves of 64 keys per query tile)
+enum { B_QFULL = 0, B_KFULL = 2, B_VFULL = 4, B_FREE = 6, B_SFULL = B_FREE + SLOTS, B_PFULL = B_SFULL + 2,
+       B_OFULL = B_PFULL + 4, B_DRAIN = B_OFULL + 2, N_BARS = B_DRAIN + 2 };
+static_assert(N_BARS * 8 <= 256, "barriers");
 constexpr uint32_t TM_S = 0, TM_O = 256;   // S_A, S_B, O_A, O_B: 128 columns each
 
 constexpr uint32_t IDESC_S = sm100::idesc_bf16(128, 128, 0, 0);
@@ -115,41 +120,89 @@ struct Args {
   int causal;
 };
 
-// Which sequence and which pair of query tiles a CTA's index means: index among the sequences'
-// pair counts, found by one warp, 32 sequences a round; a sequence's last (longest) pair first.
+// Which sequence and which pair of query tiles a CTA's index means, found by one warp. The pairs
+// of all sequences go by their number within the sequence, the last first: with causal masking
+// the longest work is then started first and the SMs finish together (sequence by sequence, 40 %
+// of their time was idle at 4,096 tokens and 16 heads). Level p holds the sequences with more
+// than p pairs; F(p), the number of pairs at level p or above, falls with p.
+__device__ __forceinline__ int pair_count(const Args& a, int n) {
+  int64_t b, e;
+  seq_bounds(a.cu_q, n, a.n_seqs, a.tq, b, e);
+  return (int)((e - b + PAIR - 1) / PAIR);
+}
 __device__ __forceinline__ void locate(const Args& a, int idx, int lane, int& n, int& pair) {
-  if (a.cu_q == nullptr) {
-    const int cnt = (int)((a.tq + PAIR - 1) / PAIR);
-    n = idx < cnt ? 0 : -1;
-    pair = cnt - 1 - idx;
-    return;
-  }
-  int base = 0;
-  for (int s0 = 0; s0 < a.n_seqs; s0 += 32) {
-    int cnt = 0;
-    if (s0 + lane < a.n_seqs) {
-      int64_t b, e;
-      seq_bounds(a.cu_q, s0 + lane, a.n_seqs, a.tq, b, e);
-      cnt = (int)((e - b + PAIR - 1) / PAIR);
-    }
-    int upto = cnt;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, off);
-      if (lane >= off) upto += v;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, idx < base + upto);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      const int c = __shfl_sync(0xffffffffu, cnt, l), u = __shfl_sync(0xffffffffu, upto, l);
-      n = s0 + l;
-      pair = c - 1 - (idx - (base + u - c));
-      return;
-    }
-    base += __shfl_sync(0xffffffffu, upto, 31);
-  }
   n = -1;
   pair = 0;
+  if (a.cu_q == nullptr) {
+    const int cnt = (int)((a.tq + PAIR - 1) / PAIR);
+    if (idx < cnt) {
+      n = 0;
+      pair = cnt - 1 - idx;
+    }
+    return;
+  }
+  const int mine = lane < a.n_seqs ? pair_count(a, lane) : 0;   // (the first 32 stay in registers)
+  auto above = [&](int p) {   // F(p)
+    int f = max(mine - p, 0);
+    for (int s = 32 + lane; s < a.n_seqs; s += 32) f += max(pair_count(a, s) - p, 0);
+    return (int)__reduce_add_sync(0xffffffffu, (unsigned)f);
+  };
+  int f1 = 0;
+  int lo = 0, hi = a.tiles;   // F(lo) > idx >= F(hi)
+  if (above(0) <= idx) return;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1, f = above(mid);
+    if (f > idx) {
+      lo = mid;
+    } else {
+      hi = mid;
+      f1 = f;
+    }
+  }
+  // of the sequences with more than lo pairs, the one at place idx - F(lo + 1)
+  int left = idx - f1;
+  for (int s0 = 0; s0 < a.n_seqs; s0 += 32) {
+    const int s = s0 + lane;
+    const unsigned b = __ballot_sync(0xffffffffu, s < a.n_seqs && (s0 == 0 ? mine : pair_count(a, s)) > lo);
+    if (left < __popc(b)) {
+      n = s0 + (int)__fns(b, 0, left + 1);
+      pair = lo;
+      return;
+    }
+    left -= __popc(b);
+  }
+}
+
+__device__ __forceinline__ float row_max(const float* s) {
+  float mx[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(s[k], s[k + 4]), s[k + 8]);
+#pragma unroll
+  for (int c = 12; c < 124; c += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], s[c + k]), s[c + k + 4]);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[124 + k]);
+  return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+
+// Weights 2^(s sc - ms) of 64 scores, as bf16 pairs, their sum added to `sum`. (Leaving every
+// fourth pair to a polynomial on the FMA units made 4,096 tokens slower, 238 against 221 us:
+// the special function unit is not what the softmax waits for.)
+__device__ __forceinline__ void weights(const float* s, float sc, float ms, uint32_t (&p)[32], float2& sum) {
+  const float2 sc2 = make_float2(sc, sc), ms2 = make_float2(-ms, -ms);
+  float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float2 x = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), sc2, ms2);
+    const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+    if (i & 1)
+      part = __fadd2_rn(part, e);
+    else
+      sum = __fadd2_rn(sum, e);
+    p[i] = pack2(e.x, e.y);
+  }
+  sum = __fadd2_rn(sum, part);
 }
 
 __global__ void __launch_bounds__(THREADS, 1)
@@ -164,15 +217,16 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
   __shared__ int s_abort, s_seq, s_pair;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int head = blockIdx.x / a.tiles;
+  const int head = blockIdx.x % a.n_heads;
   if (warp == 9) {
     int n, pair;
-    locate(a, blockIdx.x % a.tiles, lane, n, pair);
+    locate(a, blockIdx.x / a.n_heads, lane, n, pair);
     if (lane == 0) {
       s_seq = n;
       s_pair = pair;
       s_abort = 0;
-      for (int i = 0; i < N_BARS; ++i) mbar_init(&bars[i], i == B_PFULL || i == B_PFULL + 1 ? BM : 1);
+      for (int i = 0; i < N_BARS; ++i)
+        mbar_init(&bars[i], i >= B_PFULL && i < B_PFULL + 4 ? BM : i >= B_FREE && i < B_FREE + SLOTS ? 2 : 1);
       fence_mbar_init();
     }
   }
@@ -216,116 +270,116 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
     if (warp == 8) {
     // ---- copies ----
     if (lane == 0 && n_tiles > 0) {
-      int k_issued = 0, v_issued = 0;
       bool alive = true;
-      auto issue_k = [&](int j) {
-        uint64_t* full = &bars[B_KFULL + (j & 1)];
-        unsigned char* dst = sm + OFF_K + (j & 1) * K_BYTES;
-        const int y = (int)(bk + (int64_t)j * BN);
-        mbar_arrive_expect_tx(full, K_BYTES);
-        tma_load_3d(dst, &map_k, 0, head, y, full);
-        tma_load_3d(dst + BLK, &map_k, 64, head, y, full);
-        tma_load_2d(dst + 2 * BLK, &map_ks, 0, y, full);
-        ++k_issued;
+      int issued = 0;
+      auto load_q = [&](int x) {
+        if (nt[x] == 0) return;
+        const int y = (int)(bq + s_pair * PAIR + x * BM);
+        mbar_arrive_expect_tx(&bars[B_QFULL + x], Q_BYTES);
+        for (int b = 0; b < 3; ++b)
+          tma_load_3d(sm + OFF_Q + x * Q_BYTES + b * BLK, &map_q, 64 * b, head, y, &bars[B_QFULL + x]);
       };
-      for (int x = 0; x < 2; ++x) {
-        if (nt[x] > 0) {
-          const int y = (int)(bq + s_pair * PAIR + x * BM);
-          mbar_arrive_expect_tx(&bars[B_QFULL + x], Q_BYTES);
-          for (int b = 0; b < 3; ++b)
-            tma_load_3d(sm + OFF_Q + x * Q_BYTES + b * BLK, &map_q, 64 * b, head, y, &bars[B_QFULL + x]);
-        }
-        if (x == 0) issue_k(0);
-      }
-      if (n_tiles > 1) issue_k(1);
-      for (int j = 0; j < n_tiles && alive; ++j) {
-        if (j >= 1) alive = wait.one(&bars[B_VFREE], (j - 1) & 1);
-        if (!alive) break;
-        mbar_arrive_expect_tx(&bars[B_VFULL], V_BYTES);
+      load_q(0);
+      int j = 0, part = 0;   // tile, and which of its five slots
+      for (; j < n_tiles; ++issued) {
+        const int slot = issued % SLOTS, use = issued / SLOTS;
+        if (use > 0 && !(alive = wait.one(&bars[B_FREE + slot], (use - 1) & 1))) break;
+        // (a tile's keys complete one phase, its values one: every wait of the products' warp costs)
+        uint64_t* full = &bars[(part < 3 ? B_KFULL : B_VFULL) + (j & 1)];
+        unsigned char* dst = sm + OFF_RING + slot * BLK;
         const int y = (int)(bk + (int64_t)j * BN);
-        tma_load_3d(sm + OFF_V, &map_v, 0, head, y, &bars[B_VFULL]);
-        tma_load_3d(sm + OFF_V + BLK, &map_v, 64, head, y, &bars[B_VFULL]);
-        ++v_issued;
-        if (j + 2 < n_tiles) {
-          alive = wait.one(&bars[B_KFREE + (j & 1)], (j >> 1) & 1);
-          if (alive) issue_k(j + 2);
+        if (part == 0) mbar_arrive_expect_tx(full, 3 * BLK);
+        if (part == 3) mbar_arrive_expect_tx(full, 2 * BLK);
+        if (part < 2) {
+          tma_load_3d(dst, &map_k, 64 * part, head, y, full);
+        } else if (part == 2) {
+          tma_load_2d(dst, &map_ks, 0, y, full);
+          if (j == 0) load_q(1);
+        } else {
+          tma_load_3d(dst, &map_v, 0, head, y + 64 * (part - 3), full);
+          tma_load_3d(dst + BLK / 2, &map_v, 64, head, y + 64 * (part - 3), full);
+        }
+        if (++part == PER_TILE) {
+          part = 0;
+          ++j;
         }
       }
       if (!alive) {
         for (int x = 0; x < 2; ++x)
           if (nt[x] > 0) settle_bar(&bars[B_QFULL + x], 0);
-        for (int j = max(0, k_issued - 2); j < k_issued; ++j) settle_bar(&bars[B_KFULL + (j & 1)], (j >> 1) & 1);
-        if (v_issued > 0) settle_bar(&bars[B_VFULL], (v_issued - 1) & 1);
+        for (int i = max(0, j - 1); i <= j; ++i) {   // (a part of a tile leaves its phase open: the wait ends by its limit)
+          settle_bar(&bars[B_KFULL + (i & 1)], (i >> 1) & 1);
+          settle_bar(&bars[B_VFULL + (i & 1)], (i >> 1) & 1);
+        }
       }
     }
-    } else if (warp == 9) {
-    // ---- products ----
+    } else if (warp < 11) {
+    // ---- products of one query tile ----
+    // A warp each for A and B: a wait leaves its issuer's products idle for 160 to 220 cycles
+    // even when it is over at once (measured between groups of four), which the other's fill.
+    const int x = warp - 9, n_x = nt[x];
     const uint32_t sb = smem_u32(sm);
-    const uint64_t v0 = make_sdesc(sb + OFF_V, BLK, 1024, SWZ_128B);
-    bool alive = n_tiles > 0;
-    auto issue_s = [&](int x, int j) {   // S_x = Q_x K_j^T
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t q0 = make_sdesc(sb + OFF_Q + x * Q_BYTES, 16, 1024, SWZ_128B);
-        const uint64_t k0 = make_sdesc(sb + OFF_K + (j & 1) * K_BYTES, 16, 1024, SWZ_128B);
-#pragma unroll
-        for (int kk = 0; kk < 12; ++kk) {
-          const uint32_t at = ((kk >> 2) * BLK + (kk & 3) * 32) >> 4;
-          umma_bf16(tmem + TM_S + x * 128, q0 + at, k0 + at, IDESC_S, kk > 0 ? 1u : 0u);
+    const uint64_t q0 = make_sdesc(sb + OFF_Q + x * Q_BYTES, 16, 1024, SWZ_128B);
+    bool alive = n_x == 0 || wait(&bars[B_QFULL + x], 0);
+    for (int j = -1; j < n_tiles && alive; ++j) {
+      if (j >= 0) {
+        // O_x += P_x V_j, by halves of 64 keys
+        if (!(alive = wait(&bars[B_VFULL + (j & 1)], (j >> 1) & 1))) break;
+        const int valid = len_k - j * BN;
+        const int steps = j < n_x ? min(8, (kend[x] - j * BN + 15) >> 4) : 0;
+#pragma unroll 1
+        for (int h = 0; h < 2 && alive; ++h) {
+          const int slot = (j * PER_TILE + 3 + h) % SLOTS;
+          const int r0 = max(valid - 64 * h, 0), r1 = min((r0 + 15) & ~15, 64);
+          if (r0 < r1) {
+            // rows behind the sequence's last key inside its 16-row step: whatever the copy
+            // brought (the next sequence's values), their weights of zero must meet zeros
+            // (written by both warps: each before its own products)
+            unsigned char* v = sm + OFF_RING + slot * BLK;
+            for (int k = lane; k < (r1 - r0) * 16; k += 32)
+              *reinterpret_cast<uint4*>(v + ((k >> 3) & 1) * (BLK / 2) + (r0 + (k >> 4)) * 128 + (k & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (j < n_x && !(alive = wait(&bars[B_PFULL + 2 * x + h], j & 1))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t v0 = make_sdesc(sb + OFF_RING + slot * BLK, BLK / 2, 1024, SWZ_128B);
+            const int n = min(4, steps - 4 * h);
+            for (int kk = 0; kk < n; ++kk)
+              umma_bf16_tmem_a(tmem + TM_O + x * 128, tmem + TM_S + x * 128 + (4 * h + kk) * 8,
+                               v0 + ((kk * 2048) >> 4), IDESC_PV, (j > 0 || h > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(&bars[B_FREE + slot]);
+            if (h == 1 && j + 1 == n_x) umma_commit(&bars[B_OFULL + x]);
+          }
         }
-        umma_commit(&bars[B_SFULL + x]);
       }
-    };
-    alive = alive && wait(&bars[B_KFULL], 0);
-    for (int x = 0; x < 2; ++x)
-      if (nt[x] > 0) {
-        alive = alive && wait(&bars[B_QFULL + x], 0);
-        if (alive) issue_s(x, 0);
-      }
-    if (alive && elect_one()) umma_commit(&bars[B_KFREE]);
-    for (int j = 0; j < n_tiles && alive; ++j) {
-      if (!(alive = wait(&bars[B_VFULL], j & 1))) break;
-      const int valid = len_k - j * BN;
-      if (valid < BN && (valid & 15)) {
-        // rows behind the sequence's last key inside its 16-row step: whatever the copy
-        // brought (the next sequence's values), their weights of zero must meet zeros
-        const int r1 = (valid + 15) & ~15;
-        for (int i = lane; i < (r1 - valid) * 16; i += 32) {
-          const int r = valid + (i >> 4), b = (i >> 3) & 1, c = i & 7;
-          *reinterpret_cast<uint4*>(sm + OFF_V + b * BLK + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      bool have_k = false;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (j >= nt[x]) continue;
-        if (!(alive = alive && wait(&bars[B_PFULL + x], j & 1))) break;
+      // S_x(j+1) = Q_x K_j+1^T overwrites P_x(j): products of one thread run in the order of issue.
+      // (A tile of keys that x does not see any more is freed all the same.)
+      if (alive && j + 1 < n_tiles) {
+        if (!(alive = wait(&bars[B_KFULL + ((j + 1) & 1)], ((j + 1) >> 1) & 1))) break;
         tc_fence_after();
-        const int steps = min(8, (kend[x] - j * BN + 15) >> 4);
         if (elect_one()) {
-          for (int kk = 0; kk < steps; ++kk)
-            umma_bf16_tmem_a(tmem + TM_O + x * 128, tmem + TM_S + x * 128 + kk * 8, v0 + ((kk * 2048) >> 4),
-                             IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
-          if (j + 1 == nt[x]) umma_commit(&bars[B_OFULL + x]);
+#pragma unroll
+          for (int b = 0; b < 3; ++b) {
+            const int slot = ((j + 1) * PER_TILE + b) % SLOTS;
+            const uint64_t k0 = make_sdesc(sb + OFF_RING + slot * BLK, 16, 1024, SWZ_128B);
+            if (j + 1 < n_x) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_bf16(tmem + TM_S + x * 128, q0 + ((b * BLK + kk * 32) >> 4), k0 + ((kk * 32) >> 4), IDESC_S,
+                          b > 0 || kk > 0 ? 1u : 0u);
+            }
+            umma_commit(&bars[B_FREE + slot]);
+          }
+          if (j + 1 < n_x) umma_commit(&bars[B_SFULL + x]);
         }
-        if (j + 1 < nt[x]) {
-          if (!have_k) alive = wait(&bars[B_KFULL + ((j + 1) & 1)], ((j + 1) >> 1) & 1);
-          have_k = true;
-          if (!alive) break;
-          // S_x(j+1) overwrites P_x(j): products of one thread run in the order of issue
-          issue_s(x, j + 1);
-        }
-      }
-      if (alive && elect_one()) {
-        umma_commit(&bars[B_VFREE]);
-        if (j + 1 < n_tiles) umma_commit(&bars[B_KFREE + ((j + 1) & 1)]);
       }
     }
-    if (n_tiles > 0 && !alive && elect_one()) {
-      umma_commit(&bars[B_DRAIN]);
-      settle_bar(&bars[B_DRAIN], 0);
+    if (!alive && elect_one()) {
+      umma_commit(&bars[B_DRAIN + x]);
+      settle_bar(&bars[B_DRAIN + x], 0);
     }
     __syncwarp();
     }
@@ -349,54 +403,60 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
       for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, *reinterpret_cast<float(*)[32]>(&s[32 * c]));
       tmem_ld_wait();
       const int lim = see - j * BN;
-      if (__any_sync(0xffffffffu, lim < BN)) {
+      const bool masked = __any_sync(0xffffffffu, lim < BN);
+      if (masked) {
 #pragma unroll
         for (int c = 0; c < 128; ++c)
           if (c >= lim) s[c] = -INFINITY;
       }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-      for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      if (j == 0) {
-        m = mt;
-      } else {
+      // The weights of the first half are formed with the old reference while the tile's maximum
+      // is found, and again in the rare tile that moves it. (The first tile, and a masked one,
+      // find their maximum first.)
+      uint32_t p[32];
+      float2 sum = make_float2(0.f, 0.f);
+      auto move_to = [&](float mt) {   // true for the warp if a row's reference moves
         const bool move = mt > m && (mt - m) * sc > RESCALE_LOG2;   // (from -inf: always)
-        if (__any_sync(0xffffffffu, move)) {
-          // (P V of the tile before has completed: it was issued before the S waited for)
-          const float f = move ? exp2_fast((m - mt) * sc) : 1.f;
-          if (move) m = mt;
-          l *= f;
+        if (!__any_sync(0xffffffffu, move)) return false;
+        // (P V of the tile before has completed: it was issued before the S waited for)
+        const float f = move ? exp2_fast((m - mt) * sc) : 1.f;
+        if (move) m = mt;
+        l *= f;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float v[32];
-            tmem_ld32(t_o + 32 * c, v);
-            tmem_ld_wait();
+        for (int c = 0; c < 8; ++c) {
+          float v[16];
+          tmem_ld16(t_o + 16 * c, v);
+          tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= f;
-            tmem_st32(t_o + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v));
-          }
-          tmem_st_wait();
+          for (int i = 0; i < 16; ++i) v[i] *= f;
+          tmem_st16(t_o + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&v));
+        }
+        return true;
+      };
+      auto reference = [&]() { return m == -INFINITY ? 0.f : m * sc; };
+      if (j == 0 || masked) {
+        const float mt = row_max(s);
+        if (j == 0)
+          m = mt;
+        else
+          move_to(mt);
+        weights(s, sc, reference(), p, sum);
+      } else {
+        weights(s, sc, reference(), p, sum);
+        if (move_to(row_max(s))) {
+          sum = make_float2(0.f, 0.f);
+          weights(s, sc, reference(), p, sum);
         }
       }
-      const float ms = m == -INFINITY ? 0.f : m * sc;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < 128; c += 64) {
-        uint32_t p[32];
-#pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          const float e0 = exp2_fast(fmaf(s[c + i], sc, -ms)), e1 = exp2_fast(fmaf(s[c + i + 1], sc, -ms));
-          sum[i & 3] += e0;
-          sum[(i & 3) + 1] += e1;
-          p[i >> 1] = pack2(e0, e1);
-        }
-        tmem_st32(t_s + (c >> 1), p);
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_st32(t_s, p);
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&bars[B_PFULL + x]);
+      mbar_arrive(&bars[B_PFULL + 2 * x]);   // its product starts while the second half is formed
+      weights(s + 64, sc, reference(), p, sum);
+      tmem_st32(t_s + 32, p);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&bars[B_PFULL + 2 * x + 1]);
+      l += sum.x + sum.y;
     }
     if (n_x > 0 && alive) {
       alive = wait(&bars[B_OFULL + x], 0);
