@@ -349,10 +349,14 @@ template <typename TQ, typename TG>
 int launch_decode_tree(const void* q, const void* k, const void* v, const void* log_alpha,
                        const void* beta, const float* state, const int32_t* tree, void* o,
                        int32_t n_seqs, int32_t n_tokens, int32_t n_heads, cudaStream_t stream) {
+  CUtensorMap map_s;
+  if (!encode_2d(&map_s, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, state, kda::D, (uint64_t)n_seqs * n_heads * kda::D, 4, 32,
+                 kda::D, CU_TENSOR_MAP_SWIZZLE_128B))
+    return KDA_ERR_CUDA;
   const cudaError_t e = kda::launch_decode_tree<TQ, TG>(
-      static_cast<const TQ*>(q), static_cast<const TQ*>(k), static_cast<const TQ*>(v),
-      static_cast<const TG*>(log_alpha), static_cast<const TG*>(beta), state, tree,
-      static_cast<TQ*>(o), n_seqs, n_tokens, n_heads, stream);
+      map_s, static_cast<const TQ*>(q), static_cast<const TQ*>(k), static_cast<const TQ*>(v),
+      static_cast<const TG*>(log_alpha), static_cast<const TG*>(beta), tree, static_cast<TQ*>(o),
+      n_seqs, n_tokens, n_heads, stream);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 static_assert(KDA_DECODE_MAX_TOKENS == kda::TREE_MAX_TOKENS, "token limit of the ABI and the kernel");
@@ -736,7 +740,7 @@ int kda_decode_tree(const void* q, const void* k, const void* v, const void* log
       (gate_dtype != KDA_F32 && gate_dtype != KDA_BF16))
     return KDA_ERR_DTYPE;
   if (n_seqs <= 0 || n_heads <= 0 || n_tokens <= 0 || n_tokens > KDA_DECODE_MAX_TOKENS ||
-      (int64_t)n_seqs * n_heads > (int64_t)INT32_MAX)
+      (int64_t)n_seqs * n_heads > (int64_t)INT32_MAX / kda::D)   // (32-bit row coordinates of the copies)
     return KDA_ERR_SHAPE;
   if (!q || !k || !v || !log_alpha || !beta || !state || !o) return KDA_ERR_NULL;
   const void* ptrs[] = {q, k, v, log_alpha, state, o};

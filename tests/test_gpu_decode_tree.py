@@ -109,6 +109,30 @@ def test_strong_decay_and_none(kda):
     check(o, run_ref(x, state, tree)[0])
 
 
+def test_decay_between_tokens_behind_a_strong_one(kda):
+    """log alpha of -3e4 on the first token: the decay between later tokens is not lost in the
+    difference of two sums of that size (which fp32 holds to 2e-3 only)."""
+    x, state = draw(2, 2, 5, torch.float32, torch.float32, seed=345)
+    x["log_alpha"][:, 0] = -3e4
+    tree = torch.tensor([[1, 3, 7, 11, 23], [1, 3, 5, 13, 17]], dtype=torch.int32, device="cuda")
+    o = kda.decode_tree(x["q"], x["k"], x["v"], x["log_alpha"], x["beta"], state, tree)
+    check(o, run_ref(x, state, tree)[0])
+
+
+@pytest.mark.parametrize("t,dtype", [(3, torch.bfloat16), (8, torch.bfloat16), (12, torch.float32), (16, torch.bfloat16),
+                                     (16, torch.float32)])
+def test_more_states_than_resident_ctas(kda, t, dtype):
+    """Every CTA walks several states (the next one's inputs and state in flight): the batch equals
+    its parts, each small enough for one state per CTA."""
+    x, state = draw(40, 16, t, dtype, dtype, seed=347)
+    tree = ref.random_tree(40, t, seed=t + 1).cuda()
+    o = kda.decode_tree(x["q"], x["k"], x["v"], x["log_alpha"], x["beta"], state, tree)
+    for a in range(0, 40, 8):
+        part = [x[n][a:a + 8] for n in ("q", "k", "v", "log_alpha", "beta")]
+        assert torch.equal(o[a:a + 8], kda.decode_tree(*part, state[a:a + 8], tree[a:a + 8]))
+    check(o[38:], run_ref({n: y[38:] for n, y in x.items()}, state[38:], tree[38:])[0])
+
+
 def test_rows_that_are_no_path_are_flagged(kda):
     """A row with bits that are no path is taken by its parent (the highest bit below its own)
     and reported; the rest of the batch is untouched by it."""
