@@ -8,15 +8,22 @@
 //
 // One CTA takes 256 queries of one head as two tiles A and B of 128, so that one tile's softmax
 // runs while the other's products do. Warps 0-3 and 4-7 hold the softmax of A and B (thread =
-// query row, so row maxima and sums need no exchange), warp 8 issues the copies, warp 9 the
-// products. Tensor memory holds S_A, S_B (128 x 128 fp32 each) and O_A, O_B; the weights P (bf16)
-// overwrite the first half of their S and are the A operand of P V from there. Keys are double-
-// buffered in shared memory, values single: 96 + 96 + 32 KiB.
+// query row, so row maxima and sums need no exchange), warp 8 issues the copies, warps 9 and 10
+// the products of A and B. Tensor memory holds S_A, S_B (128 x 128 fp32 each) and O_A, O_B; the
+// weights P (bf16) overwrite the first half of their S and are the A operand of P V from there.
+// Queries take 96 KiB of shared memory; keys and values share a ring of eight 16 KiB slots, freed
+// one by one.
 //
 // The running reference m of a row's exponents moves only when its maximum has grown by more
-// than 8 (in powers of two): until then weights up to 2^8 are exact in the same bf16 relative
-// precision and the accumulators need no pass of their own. Maxima, sums and O are fp32; P is
-// rounded to bf16 once (half a step, 2^-8 relative per weight) as the matrix units take it.
+// than 8 (in powers of two): until then weights up to 2^8 have the same relative precision in
+// bf16 and the accumulators need no pass of their own. Maxima, sums and O are fp32; P is rounded
+// to bf16 once (half a step, 2^-8 relative per weight) as the matrix units take it.
+//
+// Measured: 4,096 tokens, 32 heads in 171 us (1.0 PFLOP/s), 32,768 tokens, 4 heads in 1.21 ms
+// (1.14), 0.62 and 0.70 of the measured bf16 rate (0.72 and 0.81 of its sustained one). A pair of
+// key tiles takes about 4,100 cycles where its products need 2,680: both tiles' chains (S,
+// softmax of 2,000 cycles, P V) run nearly in step and wait for the special function unit and the
+// tensor cores in turn.
 #pragma once
 
 #include "kda_common.cuh"
@@ -187,21 +194,27 @@ __device__ __forceinline__ float row_max(const float* s) {
   return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
 }
 
-// Weights 2^(s sc - ms) of 64 scores, as bf16 pairs, their sum added to `sum`. (Leaving every
+// Weights 2^(s sc - ms) of 64 scores, as bf16 pairs into tensor memory 16 registers at a time (32
+// made the loop spill, 2 to 3 % of its time), their sum added to `sum`. (Leaving every
 // fourth pair to a polynomial on the FMA units made 4,096 tokens slower, 238 against 221 us:
 // the special function unit is not what the softmax waits for.)
-__device__ __forceinline__ void weights(const float* s, float sc, float ms, uint32_t (&p)[32], float2& sum) {
+__device__ __forceinline__ void weights(const float* s, float sc, float ms, uint32_t t_p, float2& sum) {
   const float2 sc2 = make_float2(sc, sc), ms2 = make_float2(-ms, -ms);
   float2 part = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const float2 x = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), sc2, ms2);
-    const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
-    if (i & 1)
-      part = __fadd2_rn(part, e);
-    else
-      sum = __fadd2_rn(sum, e);
-    p[i] = pack2(e.x, e.y);
+  for (int c = 0; c < 64; c += 32) {
+    uint32_t p[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 x = __ffma2_rn(make_float2(s[c + 2 * i], s[c + 2 * i + 1]), sc2, ms2);
+      const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+      if (i & 1)
+        part = __fadd2_rn(part, e);
+      else
+        sum = __fadd2_rn(sum, e);
+      p[i] = pack2(e.x, e.y);
+    }
+    sm100::tmem_st16(t_p + (c >> 1), p);
   }
   sum = __fadd2_rn(sum, part);
 }
@@ -219,6 +232,16 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int head = blockIdx.x % a.n_heads;
+  if (warp == 8) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+    if (lane == 0 && a.tk > 0) {
+      prefetch_tensormap(&map_q);
+      prefetch_tensormap(&map_k);
+      prefetch_tensormap(&map_ks);
+      prefetch_tensormap(&map_v);
+    }
+  }
   if (warp == 9) {
     int n, pair;
     locate(a, blockIdx.x / a.n_heads, lane, n, pair);
@@ -231,9 +254,15 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
       fence_mbar_init();
     }
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
   const int seq = s_seq;
-  if (seq < 0) return;   // (the bound on the pairs counts up to one more per sequence)
+  if (seq < 0) {   // (the bound on the pairs counts up to one more per sequence)
+    if (warp == 8) tmem_dealloc(tmem, 512);
+    return;
+  }
   int64_t bq, eq, bk, ek;
   seq_bounds(a.cu_q, seq, a.n_seqs, a.tq, bq, eq);
   seq_bounds(a.cu_k, seq, a.n_seqs, a.tk, bk, ek);
@@ -248,20 +277,6 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
     nt[x] = (kend[x] + BN - 1) / BN;
   }
   const int n_tiles = max(nt[0], nt[1]);
-  if (warp == 8) {
-    tmem_alloc(&s_tmem, 512);
-    tmem_relinquish();
-    if (lane == 0 && n_tiles > 0) {
-      prefetch_tensormap(&map_q);
-      prefetch_tensormap(&map_k);
-      prefetch_tensormap(&map_ks);
-      prefetch_tensormap(&map_v);
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = s_tmem;
   const Waiter wait{&s_abort};
 
   // A softmax thread holds a row of S (128 registers): the launch's 3 x 168 registers per
@@ -269,125 +284,125 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
-    // ---- copies ----
-    if (lane == 0 && n_tiles > 0) {
-      bool alive = true;
-      int issued = 0;
-      auto load_q = [&](int x) {
-        if (nt[x] == 0) return;
-        const int y = (int)(bq + s_pair * PAIR + x * BM);
-        mbar_arrive_expect_tx(&bars[B_QFULL + x], Q_BYTES);
-        for (int b = 0; b < 3; ++b)
-          tma_load_3d(sm + OFF_Q + x * Q_BYTES + b * BLK, &map_q, 64 * b, head, y, &bars[B_QFULL + x]);
-      };
-      load_q(0);
-      int j = 0, part = 0;   // tile, and which of its five slots
-      for (; j < n_tiles; ++issued) {
-        const int slot = issued % SLOTS, use = issued / SLOTS;
-        if (use > 0 && !(alive = wait.one(&bars[B_FREE + slot], (use - 1) & 1))) break;
-        // (a tile's keys complete one phase, its values one: every wait of the products' warp costs)
-        uint64_t* full = &bars[(part < 3 ? B_KFULL : B_VFULL) + (j & 1)];
-        unsigned char* dst = sm + OFF_RING + slot * BLK;
-        const int y = (int)(bk + (int64_t)j * BN);
-        if (part == 0) mbar_arrive_expect_tx(full, 3 * BLK);
-        if (part == 3) mbar_arrive_expect_tx(full, 2 * BLK);
-        if (part < 2) {
-          tma_load_3d(dst, &map_k, 64 * part, head, y, full);
-        } else if (part == 2) {
-          tma_load_2d(dst, &map_ks, 0, y, full);
-          if (j == 0) load_q(1);
-        } else {
-          tma_load_3d(dst, &map_v, 0, head, y + 64 * (part - 3), full);
-          tma_load_3d(dst + BLK / 2, &map_v, 64, head, y + 64 * (part - 3), full);
-        }
-        if (++part == PER_TILE) {
-          part = 0;
-          ++j;
-        }
-      }
-      if (!alive) {
-        for (int x = 0; x < 2; ++x)
-          if (nt[x] > 0) settle_bar(&bars[B_QFULL + x], 0);
-        for (int i = max(0, j - 1); i <= j; ++i) {   // (a part of a tile leaves its phase open: the wait ends by its limit)
-          settle_bar(&bars[B_KFULL + (i & 1)], (i >> 1) & 1);
-          settle_bar(&bars[B_VFULL + (i & 1)], (i >> 1) & 1);
-        }
-      }
-    }
-    } else if (warp < 11) {
-    // ---- products of one query tile ----
-    // A warp each for A and B: a wait leaves its issuer's products idle for 160 to 220 cycles
-    // even when it is over at once (measured between groups of four), which the other's fill.
-    const int x = warp - 9, n_x = nt[x];
-    const uint32_t sb = smem_u32(sm);
-    const uint64_t q0 = make_sdesc(sb + OFF_Q + x * Q_BYTES, 16, 1024, SWZ_128B);
-    bool alive = n_x == 0 || wait(&bars[B_QFULL + x], 0);
-    // Over many tiles B starts when A's first weights are there, so that one tile's softmax falls
-    // into the other's products from then on: 1,255 against 1,320 us for 32,768 tokens and 4
-    // heads, 175 against 185 for 1,024 queries over 8,025 keys. Short rows lose the start (16
-    // pairs of 32 tiles at most: 190 against 184 us).
-    if (x == 1 && nt[0] >= LATE_START) alive = alive && wait(&bars[B_START], 0);
-    for (int j = -1; j < n_tiles && alive; ++j) {
-      if (j >= 0) {
-        // O_x += P_x V_j, by halves of 64 keys
-        if (!(alive = wait(&bars[B_VFULL + (j & 1)], (j >> 1) & 1))) break;
-        const int valid = len_k - j * BN;
-        const int steps = j < n_x ? min(8, (kend[x] - j * BN + 15) >> 4) : 0;
-#pragma unroll 1
-        for (int h = 0; h < 2 && alive; ++h) {
-          const int slot = (j * PER_TILE + 3 + h) % SLOTS;
-          const int r0 = max(valid - 64 * h, 0), r1 = min((r0 + 15) & ~15, 64);
-          if (r0 < r1) {
-            // rows behind the sequence's last key inside its 16-row step: whatever the copy
-            // brought (the next sequence's values), their weights of zero must meet zeros
-            // (written by both warps: each before its own products)
-            unsigned char* v = sm + OFF_RING + slot * BLK;
-            for (int k = lane; k < (r1 - r0) * 16; k += 32)
-              *reinterpret_cast<uint4*>(v + ((k >> 3) & 1) * (BLK / 2) + (r0 + (k >> 4)) * 128 + (k & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
+      // ---- copies ----
+      if (lane == 0 && n_tiles > 0) {
+        bool alive = true;
+        int issued = 0;
+        auto load_q = [&](int x) {
+          if (nt[x] == 0) return;
+          const int y = (int)(bq + s_pair * PAIR + x * BM);
+          mbar_arrive_expect_tx(&bars[B_QFULL + x], Q_BYTES);
+          for (int b = 0; b < 3; ++b)
+            tma_load_3d(sm + OFF_Q + x * Q_BYTES + b * BLK, &map_q, 64 * b, head, y, &bars[B_QFULL + x]);
+        };
+        load_q(0);
+        int j = 0, part = 0;   // tile, and which of its five slots
+        for (; j < n_tiles; ++issued) {
+          const int slot = issued % SLOTS, use = issued / SLOTS;
+          if (use > 0 && !(alive = wait.one(&bars[B_FREE + slot], (use - 1) & 1))) break;
+          // (a tile's keys complete one phase, its values one: every wait of the products' warp costs)
+          uint64_t* full = &bars[(part < 3 ? B_KFULL : B_VFULL) + (j & 1)];
+          unsigned char* dst = sm + OFF_RING + slot * BLK;
+          const int y = (int)(bk + (int64_t)j * BN);
+          if (part == 0) mbar_arrive_expect_tx(full, 3 * BLK);
+          if (part == 3) mbar_arrive_expect_tx(full, 2 * BLK);
+          if (part < 2) {
+            tma_load_3d(dst, &map_k, 64 * part, head, y, full);
+          } else if (part == 2) {
+            tma_load_2d(dst, &map_ks, 0, y, full);
+            if (j == 0) load_q(1);
+          } else {
+            tma_load_3d(dst, &map_v, 0, head, y + 64 * (part - 3), full);
+            tma_load_3d(dst + BLK / 2, &map_v, 64, head, y + 64 * (part - 3), full);
           }
-          if (j < n_x && !(alive = wait(&bars[B_PFULL + 2 * x + h], j & 1))) break;
+          if (++part == PER_TILE) {
+            part = 0;
+            ++j;
+          }
+        }
+        if (!alive) {
+          for (int x = 0; x < 2; ++x)
+            if (nt[x] > 0) settle_bar(&bars[B_QFULL + x], 0);
+          for (int i = max(0, j - 1); i <= j; ++i) {   // (a part of a tile leaves its phase open: the wait ends by its limit)
+            settle_bar(&bars[B_KFULL + (i & 1)], (i >> 1) & 1);
+            settle_bar(&bars[B_VFULL + (i & 1)], (i >> 1) & 1);
+          }
+        }
+      }
+    } else if (warp < 11) {
+      // ---- products of one query tile ----
+      // A warp each for A and B: a wait leaves its issuer's products idle for 160 to 220 cycles
+      // even when it is over at once (measured between groups of four), which the other's fill.
+      const int x = warp - 9, n_x = nt[x];
+      const uint32_t sb = smem_u32(sm);
+      const uint64_t q0 = make_sdesc(sb + OFF_Q + x * Q_BYTES, 16, 1024, SWZ_128B);
+      bool alive = n_x == 0 || wait(&bars[B_QFULL + x], 0);
+      // Over many tiles B starts when A's first weights are there, so that one tile's softmax falls
+      // into the other's products from then on: 1,255 against 1,320 us for 32,768 tokens and 4
+      // heads, 175 against 185 for 1,024 queries over 8,025 keys. Short rows lose the start (16
+      // pairs of 32 tiles at most: 190 against 184 us).
+      if (x == 1 && nt[0] >= LATE_START) alive = alive && wait(&bars[B_START], 0);
+      for (int j = -1; j < n_tiles && alive; ++j) {
+        if (j >= 0) {
+          // O_x += P_x V_j, by halves of 64 keys
+          if (!(alive = wait(&bars[B_VFULL + (j & 1)], (j >> 1) & 1))) break;
+          const int valid = len_k - j * BN;
+          const int steps = j < n_x ? min(8, (kend[x] - j * BN + 15) >> 4) : 0;
+#pragma unroll 1
+          for (int h = 0; h < 2 && alive; ++h) {
+            const int slot = (j * PER_TILE + 3 + h) % SLOTS;
+            const int r0 = max(valid - 64 * h, 0), r1 = min((r0 + 15) & ~15, 64);
+            if (r0 < r1) {
+              // rows behind the sequence's last key inside its 16-row step: whatever the copy
+              // brought (the next sequence's values), their weights of zero must meet zeros
+              // (written by both warps: each before its own products)
+              unsigned char* v = sm + OFF_RING + slot * BLK;
+              for (int k = lane; k < (r1 - r0) * 16; k += 32)
+                *reinterpret_cast<uint4*>(v + ((k >> 3) & 1) * (BLK / 2) + (r0 + (k >> 4)) * 128 + (k & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            if (j < n_x && !(alive = wait(&bars[B_PFULL + 2 * x + h], j & 1))) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t v0 = make_sdesc(sb + OFF_RING + slot * BLK, BLK / 2, 1024, SWZ_128B);
+              const int n = min(4, steps - 4 * h);
+              for (int kk = 0; kk < n; ++kk)
+                umma_bf16_tmem_a(tmem + TM_O + x * 128, tmem + TM_S + x * 128 + (4 * h + kk) * 8,
+                                 v0 + ((kk * 2048) >> 4), IDESC_PV, (j > 0 || h > 0 || kk > 0) ? 1u : 0u);
+              umma_commit(&bars[B_FREE + slot]);
+              if (h == 1 && j + 1 == n_x) umma_commit(&bars[B_OFULL + x]);
+            }
+          }
+        }
+        // S_x(j+1) = Q_x K_j+1^T overwrites P_x(j): products of one thread run in the order of issue.
+        // (A tile of keys that x does not see any more is freed all the same.)
+        if (alive && j + 1 < n_tiles) {
+          if (!(alive = wait(&bars[B_KFULL + ((j + 1) & 1)], ((j + 1) >> 1) & 1))) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t v0 = make_sdesc(sb + OFF_RING + slot * BLK, BLK / 2, 1024, SWZ_128B);
-            const int n = min(4, steps - 4 * h);
-            for (int kk = 0; kk < n; ++kk)
-              umma_bf16_tmem_a(tmem + TM_O + x * 128, tmem + TM_S + x * 128 + (4 * h + kk) * 8,
-                               v0 + ((kk * 2048) >> 4), IDESC_PV, (j > 0 || h > 0 || kk > 0) ? 1u : 0u);
-            umma_commit(&bars[B_FREE + slot]);
-            if (h == 1 && j + 1 == n_x) umma_commit(&bars[B_OFULL + x]);
-          }
-        }
-      }
-      // S_x(j+1) = Q_x K_j+1^T overwrites P_x(j): products of one thread run in the order of issue.
-      // (A tile of keys that x does not see any more is freed all the same.)
-      if (alive && j + 1 < n_tiles) {
-        if (!(alive = wait(&bars[B_KFULL + ((j + 1) & 1)], ((j + 1) >> 1) & 1))) break;
-        tc_fence_after();
-        if (elect_one()) {
 #pragma unroll
-          for (int b = 0; b < 3; ++b) {
-            const int slot = ((j + 1) * PER_TILE + b) % SLOTS;
-            const uint64_t k0 = make_sdesc(sb + OFF_RING + slot * BLK, 16, 1024, SWZ_128B);
-            if (j + 1 < n_x) {
+            for (int b = 0; b < 3; ++b) {
+              const int slot = ((j + 1) * PER_TILE + b) % SLOTS;
+              const uint64_t k0 = make_sdesc(sb + OFF_RING + slot * BLK, 16, 1024, SWZ_128B);
+              if (j + 1 < n_x) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_bf16(tmem + TM_S + x * 128, q0 + ((b * BLK + kk * 32) >> 4), k0 + ((kk * 32) >> 4), IDESC_S,
-                          b > 0 || kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < 4; ++kk)
+                  umma_bf16(tmem + TM_S + x * 128, q0 + ((b * BLK + kk * 32) >> 4), k0 + ((kk * 32) >> 4), IDESC_S,
+                            b > 0 || kk > 0 ? 1u : 0u);
+              }
+              umma_commit(&bars[B_FREE + slot]);
             }
-            umma_commit(&bars[B_FREE + slot]);
+            if (j + 1 < n_x) umma_commit(&bars[B_SFULL + x]);
           }
-          if (j + 1 < n_x) umma_commit(&bars[B_SFULL + x]);
         }
       }
-    }
-    if (!alive && elect_one()) {
-      umma_commit(&bars[B_DRAIN + x]);
-      settle_bar(&bars[B_DRAIN + x], 0);
-    }
-    __syncwarp();
+      if (!alive && elect_one()) {
+        umma_commit(&bars[B_DRAIN + x]);
+        settle_bar(&bars[B_DRAIN + x], 0);
+      }
+      __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -418,7 +433,6 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
       // The weights of the first half are formed with the old reference while the tile's maximum
       // is found, and again in the rare tile that moves it. (The first tile, and a masked one,
       // find their maximum first.)
-      uint32_t p[32];
       float2 sum = make_float2(0.f, 0.f);
       auto move_to = [&](float mt) {   // true for the warp if a row's reference moves
         const bool move = mt > m && (mt - m) * sc > RESCALE_LOG2;   // (from -inf: always)
@@ -445,21 +459,19 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
           m = mt;
         else
           move_to(mt);
-        weights(s, sc, reference(), p, sum);
+        weights(s, sc, reference(), t_s, sum);
       } else {
-        weights(s, sc, reference(), p, sum);
+        weights(s, sc, reference(), t_s, sum);
         if (move_to(row_max(s))) {
           sum = make_float2(0.f, 0.f);
-          weights(s, sc, reference(), p, sum);
+          weights(s, sc, reference(), t_s, sum);
         }
       }
-      tmem_st32(t_s, p);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&bars[B_PFULL + 2 * x]);   // its product starts while the second half is formed
       if (x == 0 && j == 0) mbar_arrive(&bars[B_START]);
-      weights(s + 64, sc, reference(), p, sum);
-      tmem_st32(t_s + 32, p);
+      weights(s + 64, sc, reference(), t_s + 32, sum);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&bars[B_PFULL + 2 * x + 1]);
