@@ -8,8 +8,8 @@
 //
 // One CTA takes 256 queries of one head as two tiles A and B of 128, so that one tile's softmax
 // runs while the other's products do. Warps 0-3 and 4-7 hold the softmax of A and B (thread =
-// query row, so row maxima and sums need no exchange), warp 8 issues the copies, warps 9 and 10
-// the products of A and B. Tensor memory holds S_A, S_B (128 x 128 fp32 each) and O_A, O_B; the
+// query row, so row maxima and sums need no exchange), warps 8 and 11 issue the copies, warps 9 and
+// 10 the products of A and B. Tensor memory holds S_A, S_B (128 x 128 fp32 each) and O_A, O_B; the
 // weights P (bf16) overwrite the first half of their S and are the A operand of P V from there.
 // Queries take 96 KiB of shared memory; keys and values share a ring of eight 16 KiB slots, freed
 // one by one.
@@ -98,7 +98,7 @@ constexpr int BM = 128;             // queries per tile
 constexpr int PAIR = 2 * BM;        // queries per CTA
 constexpr int LATE_START = 40;      // key tiles from which on tile B starts behind A
 constexpr int BN = 128;             // keys per tile
-constexpr int THREADS = 384;        // (warp 11 idle: registers are split by groups of four)
+constexpr int THREADS = 384;
 constexpr uint32_t BLK = 128 * 128; // 16 KiB: a 128-row block of 64 bf16 columns
 constexpr uint32_t Q_BYTES = 3 * BLK;
 constexpr int SLOTS = 8;            // keys and values pass through a ring of 16 KiB slots: a tile's
@@ -283,11 +283,12 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
   // thread of the three warpgroups are split 208 + 208 + 88.
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 8) {
-      // ---- copies ----
+    if (warp == 8 || warp == 11) {
+      // ---- copies: warp 8 queries and keys, warp 11 values (each waits for its own slots) ----
       if (lane == 0 && n_tiles > 0) {
+        const bool keys = warp == 8;
         bool alive = true;
-        int issued = 0;
+        int j = 0;
         auto load_q = [&](int x) {
           if (nt[x] == 0) return;
           const int y = (int)(bq + s_pair * PAIR + x * BM);
@@ -295,38 +296,33 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
           for (int b = 0; b < 3; ++b)
             tma_load_3d(sm + OFF_Q + x * Q_BYTES + b * BLK, &map_q, 64 * b, head, y, &bars[B_QFULL + x]);
         };
-        load_q(0);
-        int j = 0, part = 0;   // tile, and which of its five slots
-        for (; j < n_tiles; ++issued) {
-          const int slot = issued % SLOTS, use = issued / SLOTS;
-          if (use > 0 && !(alive = wait.one(&bars[B_FREE + slot], (use - 1) & 1))) break;
-          // (a tile's keys complete one phase, its values one: every wait of the products' warp costs)
-          uint64_t* full = &bars[(part < 3 ? B_KFULL : B_VFULL) + (j & 1)];
-          unsigned char* dst = sm + OFF_RING + slot * BLK;
+        if (keys) load_q(0);
+        for (; j < n_tiles && alive; ++j) {
           const int y = (int)(bk + (int64_t)j * BN);
-          if (part == 0) mbar_arrive_expect_tx(full, 3 * BLK);
-          if (part == 3) mbar_arrive_expect_tx(full, 2 * BLK);
-          if (part < 2) {
-            tma_load_3d(dst, &map_k, 64 * part, head, y, full);
-          } else if (part == 2) {
-            tma_load_2d(dst, &map_ks, 0, y, full);
-            if (j == 0) load_q(1);
-          } else {
-            tma_load_3d(dst, &map_v, 0, head, y + 64 * (part - 3), full);
-            tma_load_3d(dst + BLK / 2, &map_v, 64, head, y + 64 * (part - 3), full);
-          }
-          if (++part == PER_TILE) {
-            part = 0;
-            ++j;
+          // (a tile's keys complete one phase, its values one: every wait of the products' warps costs)
+          uint64_t* full = &bars[(keys ? B_KFULL : B_VFULL) + (j & 1)];
+          for (int part = keys ? 0 : 3; part < (keys ? 3 : PER_TILE); ++part) {
+            const int i = j * PER_TILE + part, slot = i % SLOTS, use = i / SLOTS;
+            if (use > 0 && !(alive = wait.one(&bars[B_FREE + slot], (use - 1) & 1))) break;
+            unsigned char* dst = sm + OFF_RING + slot * BLK;
+            if (part == 0) mbar_arrive_expect_tx(full, 3 * BLK);
+            if (part == 3) mbar_arrive_expect_tx(full, 2 * BLK);
+            if (part < 2) {
+              tma_load_3d(dst, &map_k, 64 * part, head, y, full);
+            } else if (part == 2) {
+              tma_load_2d(dst, &map_ks, 0, y, full);
+              if (j == 0) load_q(1);
+            } else {
+              tma_load_3d(dst, &map_v, 0, head, y + 64 * (part - 3), full);
+              tma_load_3d(dst + BLK / 2, &map_v, 64, head, y + 64 * (part - 3), full);
+            }
           }
         }
         if (!alive) {
           for (int x = 0; x < 2; ++x)
-            if (nt[x] > 0) settle_bar(&bars[B_QFULL + x], 0);
-          for (int i = max(0, j - 1); i <= j; ++i) {   // (a part of a tile leaves its phase open: the wait ends by its limit)
-            settle_bar(&bars[B_KFULL + (i & 1)], (i >> 1) & 1);
-            settle_bar(&bars[B_VFULL + (i & 1)], (i >> 1) & 1);
-          }
+            if (keys && nt[x] > 0) settle_bar(&bars[B_QFULL + x], 0);
+          for (int i = max(0, j - 2); i <= j; ++i)   // (a part of a tile leaves its phase open: the wait ends by its limit)
+            settle_bar(&bars[(keys ? B_KFULL : B_VFULL) + (i & 1)], (i >> 1) & 1);
         }
       }
     } else if (warp < 11) {
