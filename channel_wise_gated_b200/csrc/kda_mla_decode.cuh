@@ -22,6 +22,12 @@
 // lengths and few long sequences fill the GPU alike. A run covers parts of one or more
 // (sequence, row group) items; an item cut by a run's border is left as partial sums (fp32) in
 // the workspace and joined by a second kernel in a fixed order.
+//
+// Measured: 128 sequences of 1k to 8k rows, 32 heads, one token: 134 to 153 us by clock (721 MB; a
+// read of them alone takes 121). Per tile of 32 keys S takes 36 products of 27 cycles (64 x 32 x
+// 16: the operands' reads, not the multiplications), P V 8 of 43 (32 rows) to 50 (64); copies of
+// the stages not held by products keep about 110 KiB in flight per SM. 48 trees of 8 tokens (256
+// rows a sequence, four items that share the cache in L2): 203 to 234 us, bound by S.
 #pragma once
 
 #include "kda_common.cuh"
