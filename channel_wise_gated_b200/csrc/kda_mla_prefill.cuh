@@ -128,35 +128,24 @@ struct Args {
   int causal;
 };
 
-// Which sequence and which pair of query tiles a CTA's index means, found by one warp. The pairs
-// of all sequences go by their number within the sequence, the last first: with causal masking
-// the longest work is then started first and the SMs finish together (sequence by sequence, 40 %
-// of their time was idle at 4,096 tokens and 16 heads). Level p holds the sequences with more
-// than p pairs; F(p), the number of pairs at level p or above, falls with p.
+// Which sequence and which pair of query tiles a CTA's index means (n = -1: none).
 __device__ __forceinline__ int pair_count(const Args& a, int n) {
   int64_t b, e;
   seq_bounds(a.cu_q, n, a.n_seqs, a.tq, b, e);
   return (int)((e - b + PAIR - 1) / PAIR);
 }
-__device__ __forceinline__ void locate(const Args& a, int idx, int lane, int& n, int& pair) {
+// Up to 32 sequences, by one warp: the pairs of all sequences go by their number within the
+// sequence, the last first. With causal masking the longest work is then started first and the
+// SMs finish together (sequence by sequence, 40 % of their time was idle at 4,096 tokens and 16
+// heads). Level p holds the sequences with more than p pairs; F(p), the number of pairs at level p
+// or above, falls with p.
+__device__ __forceinline__ void locate_by_level(const Args& a, int idx, int lane, int& n, int& pair) {
   n = -1;
   pair = 0;
-  if (a.cu_q == nullptr) {
-    const int cnt = (int)((a.tq + PAIR - 1) / PAIR);
-    if (idx < cnt) {
-      n = 0;
-      pair = cnt - 1 - idx;
-    }
-    return;
-  }
-  const int mine = lane < a.n_seqs ? pair_count(a, lane) : 0;   // (the first 32 stay in registers)
-  auto above = [&](int p) {   // F(p)
-    int f = max(mine - p, 0);
-    for (int s = 32 + lane; s < a.n_seqs; s += 32) f += max(pair_count(a, s) - p, 0);
-    return (int)__reduce_add_sync(0xffffffffu, (unsigned)f);
-  };
-  int f1 = 0;
-  int lo = 0, hi = a.tiles;   // F(lo) > idx >= F(hi)
+  const int mine = a.cu_q == nullptr ? (lane == 0 ? (int)((a.tq + PAIR - 1) / PAIR) : 0)
+                                     : (lane < a.n_seqs ? pair_count(a, lane) : 0);
+  auto above = [&](int p) { return (int)__reduce_add_sync(0xffffffffu, (unsigned)max(mine - p, 0)); };
+  int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu, (unsigned)mine), f1 = 0;   // F(lo) > idx >= F(hi) = f1
   if (above(0) <= idx) return;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1, f = above(mid);
@@ -168,17 +157,39 @@ __device__ __forceinline__ void locate(const Args& a, int idx, int lane, int& n,
     }
   }
   // of the sequences with more than lo pairs, the one at place idx - F(lo + 1)
-  int left = idx - f1;
-  for (int s0 = 0; s0 < a.n_seqs; s0 += 32) {
-    const int s = s0 + lane;
-    const unsigned b = __ballot_sync(0xffffffffu, s < a.n_seqs && (s0 == 0 ? mine : pair_count(a, s)) > lo);
-    if (left < __popc(b)) {
-      n = s0 + (int)__fns(b, 0, left + 1);
-      pair = lo;
-      return;
-    }
-    left -= __popc(b);
+  n = (int)__fns(__ballot_sync(0xffffffffu, mine > lo), 0, idx - f1 + 1);
+  pair = lo;
+}
+// More sequences, by the whole block: sequence by sequence, a sequence's last pair first (with that
+// many, the items even out by themselves, and the search stays one pass over the lengths).
+__device__ __forceinline__ void locate_in_order(const Args& a, int idx, int (&sums)[THREADS / 32], int& n_out, int& pair_out) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.n_seqs + THREADS - 1) / THREADS;
+  const int n0 = min(a.n_seqs, tid * per), n1 = min(a.n_seqs, n0 + per);
+  int mine = 0;
+  for (int n = n0; n < n1; ++n) mine += pair_count(a, n);
+  int upto = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += v;
   }
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  int before = upto - mine;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w)
+    if (w < warp) before += sums[w];
+  if (idx >= before && idx < before + mine)
+    for (int n = n0; n < n1; ++n) {
+      const int c = pair_count(a, n);
+      if (idx < before + c) {
+        n_out = n;
+        pair_out = c - 1 - (idx - before);
+        break;
+      }
+      before += c;
+    }
 }
 
 __device__ __forceinline__ float row_max(const float* s) {
@@ -228,7 +239,7 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
   unsigned char* sm = pf_smem_raw + ((1024u - (smem_u32(pf_smem_raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_seq, s_pair;
+  __shared__ int s_abort, s_seq, s_pair, s_sums[THREADS / 32];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int head = blockIdx.x % a.n_heads;
@@ -243,8 +254,8 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
     }
   }
   if (warp == 9) {
-    int n, pair;
-    locate(a, blockIdx.x / a.n_heads, lane, n, pair);
+    int n = -1, pair = 0;
+    if (a.n_seqs <= 32) locate_by_level(a, blockIdx.x / a.n_heads, lane, n, pair);
     if (lane == 0) {
       s_seq = n;
       s_pair = pair;
@@ -254,6 +265,8 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
       fence_mbar_init();
     }
   }
+  // (s_seq is set above before the search's own barrier, so a hit below comes after it)
+  if (a.n_seqs > 32) locate_in_order(a, blockIdx.x / a.n_heads, s_sums, s_seq, s_pair);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -172,3 +172,48 @@ def test_calls_on_two_streams_at_once(kda):
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(g, want[i]) for g in got[i])
+
+
+@pytest.mark.parametrize("N", [33, 700, 3001])
+def test_many_short_sequences(kda, N):
+    """Packed batches of thousands of sequences, some empty: appended, attended in both forms. Every
+    sequence's result is that of a small batch of it and its neighbours."""
+    torch.manual_seed(4)
+    page, H = 8, 2
+    g = torch.Generator().manual_seed(N)
+    lens = torch.randint(0, 6, (N,), generator=g).tolist()
+    lens[5], lens[N - 1] = 300, 270
+    cu = [0]
+    for x in lens:
+        cu.append(cu[-1] + x)
+    T = cu[-1]
+    need = [-(-x // page) for x in lens]
+    table = torch.zeros(N, max(need), dtype=torch.int32)
+    at = 0
+    for n, k in enumerate(need):
+        table[n, :k] = torch.arange(at, at + k)
+        at += k
+    table = table.cuda()
+    cache = torch.zeros(at, page, W, device="cuda", dtype=torch.bfloat16)
+    x = torch.randn(T, W, device="cuda").bfloat16()
+    kda.mla_append(x, None, cache, table, i32(lens), cu_seqlens=i32(cu))
+    for n in (0, 5, N // 2, N - 1):
+        rows = cache[table[n, :need[n]].long()].reshape(-1, W)[:lens[n]]
+        assert torch.equal(rows, x[cu[n]:cu[n + 1]])
+    q = torch.randn(T, H, D + SH, device="cuda").bfloat16()
+    k, v = torch.randn(T, H, D, device="cuda").bfloat16(), torch.randn(T, H, D, device="cuda").bfloat16()
+    o, lse = kda.mla_prefill(q, k, x[:, LAT:], v, cu_seqlens=i32(cu), output_lse=True)
+    qd = (torch.randn(N, 1, H, W, device="cuda") * 0.577).bfloat16()
+    od, ld = kda.mla_decode(qd, cache, table, i32(lens), output_lse=True)
+    for a in (0, N // 2 - 3, N - 9):
+        b = a + 9
+        s, e = cu[a], cu[b]
+        part = i32([c - s for c in cu[a:b + 1]])
+        o1, l1 = kda.mla_prefill(q[s:e], k[s:e], x[s:e, LAT:], v[s:e], cu_seqlens=part, output_lse=True)
+        assert torch.equal(o[s:e], o1) and torch.equal(lse[s:e], l1)
+        od1, ld1 = kda.mla_decode(qd[a:b].contiguous(), cache, table[a:b].contiguous(), i32(lens[a:b]), output_lse=True)
+        # (a run's border may cut a long one elsewhere: fp32 sums in another order)
+        fin = torch.isfinite(ld1)
+        assert torch.equal(fin, torch.isfinite(ld[a:b]))
+        assert float((ld[a:b] - ld1)[fin].abs().max()) <= 1e-5 * 10
+        assert float((od[a:b].float() - od1.float()).abs().max()) <= 2 ** -7 * float(od1.float().abs().max())
