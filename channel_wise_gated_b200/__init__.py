@@ -385,28 +385,32 @@ def decode_tree(q, k, v, log_alpha, beta, state, tree=None, o=None):
     return o
 
 
-def _need_rows(t, name, dtype, shape, device):
-    """As _need, for tensors whose last dimension alone must be dense: the strides of the others
-    are passed on, in multiples of 8 elements (16 bytes of bf16)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
+def _rows(t, name, dtype, shape, device):
+    """Check a tensor whose last dimension alone must be dense; returns its pointer and the other
+    dimensions' strides, which are passed on (multiples of 8 elements, 16 bytes of bf16; of a
+    dimension of one entry, where torch may report any, the dense one)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == shape
+            and (device is None or t.device == device)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if device is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.is_contiguous() and all(n % 8 == 0 for n in t.shape[1:]):
-        return
-    if t.stride(-1) != 1 or any(s % 8 for n, s in zip(t.shape, t.stride()[:-1]) if n > 1):
+    strides = t.stride()
+    dense, odd, out = shape[-1], strides[-1] != 1, []
+    for n, s in zip(shape[-2::-1], strides[-2::-1]):
+        if n <= 1:
+            s = dense
+        odd = odd or s % 8
+        out.append(s)
+        dense = n * s
+    if odd:
         raise ValueError(f"{name} must have a dense last dimension and strides in multiples of 8")
-
-
-def _row_stride(t, dim, dense):
-    """The stride of dimension dim; of one entry, where torch may report any, the dense one."""
-    return t.stride(dim) if t.shape[dim] > 1 else dense
+    return (t.data_ptr(), *out[::-1])
 
 
 def _paged_cache(cache, page_table, cache_lens, n_seqs, dev):
@@ -436,7 +440,7 @@ def mla_append(x, norm_w, cache, page_table, cache_lens, cu_seqlens=None, latent
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be [T, 576]")
     dev, T = x.device, x.shape[0]
-    _need_rows(x, "x", torch.bfloat16, (T, MLA_WIDTH), None)
+    xs = _rows(x, "x", torch.bfloat16, (T, MLA_WIDTH), None)
     _need(cache_lens, "cache_lens", torch.int32, None, dev)
     N = cache_lens.numel()
     n_pages, page_size, max_pages = _paged_cache(cache, page_table, cache_lens, N, dev)
@@ -448,8 +452,7 @@ def mla_append(x, norm_w, cache, page_table, cache_lens, cu_seqlens=None, latent
         _need(latent, "latent", torch.bfloat16, (T, MLA_LATENT), dev)
     elif output_latent:
         latent = torch.empty((T, MLA_LATENT), dtype=torch.bfloat16, device=dev)
-    _launch(lib.kda_mla_append, "kda_mla_append", dev, _ptr(x), _row_stride(x, 0, MLA_WIDTH),
-            _ptr(norm_w), float(eps), _ptr(cache), n_pages, page_size, _ptr(page_table), max_pages,
+    _launch(lib.kda_mla_append, "kda_mla_append", dev, *xs, _ptr(norm_w), float(eps), _ptr(cache), n_pages, page_size, _ptr(page_table), max_pages,
             _ptr(cache_lens), _ptr(cu_seqlens), N, T, _ptr(latent))
     return latent
 
@@ -471,21 +474,22 @@ def mla_prefill(q, k, k_shared, v, cu_seqlens=None, cu_seqlens_k=None, scale=Non
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must be [Tk, H, 128]")
     dev, (Tq, H, _), Tk = q.device, q.shape, k.shape[0]
-    _need_rows(q, "q", torch.bfloat16, (Tq, H, D + MLA_SHARED), None)
-    _need_rows(k, "k", torch.bfloat16, (Tk, H, D), dev)
-    _need_rows(v, "v", torch.bfloat16, (Tk, H, D), dev)
-    _need_rows(k_shared, "k_shared", torch.bfloat16, (Tk, MLA_SHARED), dev)
+    qs = _rows(q, "q", torch.bfloat16, (Tq, H, D + MLA_SHARED), None)
+    k_ = _rows(k, "k", torch.bfloat16, (Tk, H, D), dev)
+    vs = _rows(v, "v", torch.bfloat16, (Tk, H, D), dev)
+    shs = _rows(k_shared, "k_shared", torch.bfloat16, (Tk, MLA_SHARED), dev)
     N = 1
     if cu_seqlens is not None:
         _need(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens must be [N+1]")
         N = cu_seqlens.numel() - 1
-        if cu_seqlens_k is None:
-            if Tk != Tq:
-                raise ValueError("cu_seqlens_k is needed where queries and keys differ in number")
+        if cu_seqlens_k is not None:
+            _need(cu_seqlens_k, "cu_seqlens_k", torch.int32, (N + 1,), dev)
+        elif Tk != Tq:
+            raise ValueError("cu_seqlens_k is needed where queries and keys differ in number")
+        else:
             cu_seqlens_k = cu_seqlens
-        _need(cu_seqlens_k, "cu_seqlens_k", torch.int32, (N + 1,), dev)
     elif cu_seqlens_k is not None:
         raise ValueError("cu_seqlens_k needs cu_seqlens")
     if o is None:
@@ -495,16 +499,11 @@ def mla_prefill(q, k, k_shared, v, cu_seqlens=None, cu_seqlens_k=None, scale=Non
     if lse is not None:
         _need(lse, "lse", torch.float32, (Tq, H), dev)
     elif output_lse:
-        lse = torch.empty((Tq, H), dtype=torch.float32, device=dev)
+        lse = q.new_empty((Tq, H), dtype=torch.float32)
     if scale is None:
         scale = (D + MLA_SHARED) ** -0.5
 
-    def strides(t, width):
-        th = _row_stride(t, 1, width)
-        return _ptr(t), _row_stride(t, 0, H * th), th
-
-    _launch(lib.kda_mla_prefill, "kda_mla_prefill", dev, *strides(q, D + MLA_SHARED), *strides(k, D),
-            _ptr(k_shared), _row_stride(k_shared, 0, MLA_SHARED), *strides(v, D), _ptr(cu_seqlens),
+    _launch(lib.kda_mla_prefill, "kda_mla_prefill", dev, *qs, *k_, *shs, *vs, _ptr(cu_seqlens),
             _ptr(cu_seqlens_k), N, Tq, Tk, H, float(scale), int(causal), _ptr(o), _ptr(lse))
     return o, lse
 
@@ -552,11 +551,11 @@ def mla_decode(q, cache, page_table, cache_lens, tree=None, scale=None, o=None, 
     if lse is not None:
         _need(lse, "lse", torch.float32, (N, t, H), dev)
     elif output_lse:
-        lse = torch.empty((N, t, H), dtype=torch.float32, device=dev)
+        lse = q.new_empty((N, t, H), dtype=torch.float32)
     if scale is None:
         scale = (D + MLA_SHARED) ** -0.5
     if workspace is None:
-        workspace = torch.empty(mla_decode_workspace_size(t, H, dev), dtype=torch.uint8, device=dev)
+        workspace = q.new_empty(mla_decode_workspace_size(t, H, dev), dtype=torch.uint8)
     else:
         _need(workspace, "workspace", torch.uint8, None, dev)
     _launch(lib.kda_mla_decode, "kda_mla_decode", dev, _ptr(q), _ptr(cache), n_pages, page_size,
