@@ -887,7 +887,7 @@ int kda_mla_decode(const void* q, const void* cache, int64_t n_pages, int32_t pa
   a.max_pages = max_pages;
   a.page_rows = std::min(page_size & -page_size, BN);
   const int64_t line = (int64_t)n_seqs * a.groups * (((int64_t)max_pages * page_size + BN - 1) / BN);
-  a.grid = (int)std::min<int64_t>(sms, line);
+  a.grid = (int)std::min<int64_t>(std::min(sms, MAX_GRID), line);
   a.scale = scale;
   CUtensorMap mq, mc;
   const uint64_t qd[3] = {64, (uint64_t)n_seqs * a.rows, WIDTH / 64}, qs[2] = {WIDTH * 2, 128};

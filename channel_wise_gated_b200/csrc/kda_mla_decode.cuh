@@ -50,6 +50,7 @@ constexpr int LOOK = 4;                                 // tiles from reading a 
 // 20.4 us with 2 (more parts to join, and no idle SM for the join to start on), 12.1 / 14.8 / 17.6
 // with 3, 12.9 / 15.3 / 16.7 with 4.
 constexpr int MIN_TILES = 3;
+constexpr int MAX_GRID = 160;                           // CTAs of the main kernel at most (the join holds a part per lane and round)
 enum { B_KVFULL = 0, B_KVFREE = MAX_STAGES, B_SFULL = 2 * MAX_STAGES, B_PFULL = B_SFULL + 8, B_PVDONE = B_PFULL + 2,
        B_QFULL = B_PVDONE + 2, B_QFREE, B_OFREE, B_DRAIN, N_BARS = B_DRAIN + 2 };
 constexpr uint32_t TM_O = 0, TM_S = 256;                // four accumulators 64 columns apart; eight S
@@ -212,25 +213,7 @@ kda_mla_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
   __shared__ int64_t s_sums[THREADS / 32], s_found[2];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // sequences without keys: zeros and -inf, spread over the CTAs
-  for (int n = blockIdx.x; n < a.n_seqs; n += gridDim.x)
-    if (seq_len(a, n, tid == 0) == 0) {
-      const int64_t r0 = (int64_t)n * a.rows;
-      uint4* od = reinterpret_cast<uint4*>(a.o + r0 * LATENT);
-      for (int64_t i = tid; i < (int64_t)a.rows * (LATENT / 8); i += THREADS) od[i] = make_uint4(0, 0, 0, 0);
-      if (a.lse)
-        for (int i = tid; i < a.rows; i += THREADS) a.lse[r0 + i] = -INFINITY;
-    }
-  int workers, n_at;
-  int64_t begin, end, first_at;
-  locate<THREADS>(a, s_sums, s_found, blockIdx.x, workers, begin, end, n_at, first_at);
-  if (begin >= end) return;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the join waits for this kernel's end)
-  if (tid == 0) {
-    s_abort = 0;
-    for (int i = 0; i < N_BARS; ++i) mbar_init(&bars[i], i == B_PFULL || i == B_PFULL + 1 || i == B_OFREE ? 128 : 1);
-    fence_mbar_init();
-  }
+  // (what needs no lengths goes out before they are loaded: a short call is all latency)
   if (warp == 4) {
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
@@ -239,13 +222,21 @@ kda_mla_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
       prefetch_tensormap(&map_c);
     }
   }
+  if (tid == 0) {
+    s_abort = 0;
+    for (int i = 0; i < N_BARS; ++i) mbar_init(&bars[i], i == B_PFULL || i == B_PFULL + 1 || i == B_OFREE ? 128 : 1);
+    fence_mbar_init();
+  }
   tc_fence_before();
-  __syncthreads();
+  int workers, n_at;
+  int64_t begin, end, first_at;
+  locate<THREADS>(a, s_sums, s_found, blockIdx.x, workers, begin, end, n_at, first_at);   // (with its barriers)
   tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the join waits for this kernel's end)
   const uint32_t tmem = s_tmem;
   const Waiter wait{&s_abort};
   Walk w;
-  bool more = w.start(a, n_at, first_at, begin, end);
+  bool more = w.start(a, n_at, first_at, begin, end);   // (false for a CTA without a run: every role passes)
 
   if (warp == 4) {
     // ---- copies: lane c brings the c-th piece of page_rows rows of a tile ----
@@ -555,6 +546,15 @@ kda_mla_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
       mbar_arrive(&bars[B_OFREE]);
     }
   }
+  // sequences without keys: zeros and -inf, spread over the CTAs
+  for (int n = blockIdx.x; n < a.n_seqs; n += gridDim.x)
+    if (seq_len(a, n, tid == 0) == 0) {
+      const int64_t r0 = (int64_t)n * a.rows;
+      uint4* od = reinterpret_cast<uint4*>(a.o + r0 * LATENT);
+      for (int64_t i = tid; i < (int64_t)a.rows * (LATENT / 8); i += THREADS) od[i] = make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (int i = tid; i < a.rows; i += THREADS) a.lse[r0 + i] = -INFINITY;
+    }
   tc_fence_before();
   __syncthreads();
   if (warp == 4) {
@@ -580,7 +580,6 @@ kda_mla_decode_join_kernel(const Args a, int by_item) {
   __shared__ int64_t s_sums[JOIN_WARPS], s_found[2], s_mine[JOIN_WARPS];
   constexpr int SPAN = ALONE ? 4 : 1;   // 16-byte pieces of a row per lane
   __shared__ float4 s_acc[ALONE ? 1 : JOIN_WARPS / 2][32];
-  __shared__ float s_l[JOIN_WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int workers, n, g, tiles;
   int64_t begin, end, first_at, total, f;
@@ -634,38 +633,64 @@ kda_mla_decode_join_kernel(const Args a, int by_item) {
   const int c0 = ALONE ? 0 : 32 * ((int)blockIdx.y & 3);   // first piece
   if (r >= min(a.rb, a.rows - g * a.rb)) return;   // (not ALONE: the same for the whole block)
 
-  // row of the part that worker b left: its second slot if the item begins in it, else its first
-  const float* ml = a.part + (int64_t)2 * a.grid * a.rb * LATENT;
-  auto row_of = [&](int b) { return (int64_t)(2 * b + (b == b0)) * a.rb + r; };
-  float m = -INFINITY;
-  for (int b = b0 + lane; b <= b1; b += 32) m = fmaxf(m, ml[row_of(b) * 2]);
+  // Row of the k-th part, which worker b0 + k left: in its second slot if the item begins in it,
+  // else its first. All parts' maxima and sums come in one round of loads, lane by lane, and with
+  // them the first part's sums.
+  const int parts = b1 - b0 + 1;
+  const float2* ml = reinterpret_cast<const float2*>(a.part + (int64_t)2 * a.grid * a.rb * LATENT);
+  auto row_of = [&](int k) { return (int64_t)(2 * (b0 + k) + (k == 0)) * a.rb + r; };
+  constexpr int MOST = (MAX_GRID + 31) / 32, STEP = ALONE ? 1 : JOIN_WARPS;
+  const int k0 = ALONE ? 0 : warp;
+  float2 v[MOST];
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    const int k = 32 * i + lane;
+    v[i] = k < parts ? ml[row_of(k)] : make_float2(-INFINITY, 0.f);
+  }
+  float4 ahead[SPAN];
+#pragma unroll
+  for (int c = 0; c < SPAN; ++c)
+    ahead[c] = k0 < parts ? reinterpret_cast<const float4*>(a.part + row_of(k0) * LATENT)[c0 + 32 * c + lane]
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) m = fmaxf(m, v[i].x);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   const float ms = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    v[i].x = exp2_fast(v[i].x - ms);   // the part's weight
+    l = fmaf(v[i].x, v[i].y, l);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
   float4 acc[SPAN];
+  {
+    const float w = __shfl_sync(0xffffffffu, v[0].x, k0);
 #pragma unroll
-  for (int k = 0; k < SPAN; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int STEP = ALONE ? 1 : JOIN_WARPS;
-#pragma unroll (ALONE ? 3 : 8)
-  for (int b = b0 + (ALONE ? 0 : warp); b <= b1; b += STEP) {
-    const int64_t row = row_of(b);
-    const float w = exp2_fast(ml[row * 2] - ms);
-    const float4* src = reinterpret_cast<const float4*>(a.part + row * LATENT);
-    l = fmaf(w, ml[row * 2 + 1], l);
+    for (int c = 0; c < SPAN; ++c) acc[c] = make_float4(w * ahead[c].x, w * ahead[c].y, w * ahead[c].z, w * ahead[c].w);
+  }
 #pragma unroll
-    for (int k = 0; k < SPAN; ++k) {
-      const float4 v = src[c0 + 32 * k + lane];
-      acc[k].x = fmaf(w, v.x, acc[k].x);
-      acc[k].y = fmaf(w, v.y, acc[k].y);
-      acc[k].z = fmaf(w, v.z, acc[k].z);
-      acc[k].w = fmaf(w, v.w, acc[k].w);
+  for (int i = 0; i < MOST; ++i) {
+    const int last = min(parts, 32 * i + 32);
+#pragma unroll 4
+    for (int k = 32 * i + k0 + (i == 0 ? STEP : 0); k < last; k += STEP) {
+      const float w = __shfl_sync(0xffffffffu, v[i].x, k & 31);
+      const float4* src = reinterpret_cast<const float4*>(a.part + row_of(k) * LATENT);
+#pragma unroll
+      for (int c = 0; c < SPAN; ++c) {
+        const float4 x = src[c0 + 32 * c + lane];
+        acc[c].x = fmaf(w, x.x, acc[c].x);
+        acc[c].y = fmaf(w, x.y, acc[c].y);
+        acc[c].z = fmaf(w, x.z, acc[c].z);
+        acc[c].w = fmaf(w, x.w, acc[c].w);
+      }
     }
   }
   const int64_t row = (int64_t)n * a.rows + g * a.rb + r;
   uint2* od = reinterpret_cast<uint2*>(a.o + row * LATENT);
   if constexpr (!ALONE) {
-    if (lane == 0) s_l[warp] = l;
 #pragma unroll
     for (int half = JOIN_WARPS / 2; half > 0; half >>= 1) {   // the upper half's sums onto the lower's
       if (warp >= half && warp < 2 * half) s_acc[warp - half][lane] = acc[0];
@@ -680,9 +705,6 @@ kda_mla_decode_join_kernel(const Args a, int by_item) {
       __syncthreads();
     }
     if (warp != 0) return;
-    l = 0.f;
-#pragma unroll
-    for (int k = 0; k < JOIN_WARPS; ++k) l += s_l[k];
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
