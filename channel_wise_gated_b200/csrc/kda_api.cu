@@ -415,7 +415,7 @@ bool stride_ok(int64_t s, int64_t least) {
 int validate_cache(const void* cache, int64_t n_pages, int32_t page_size, const int32_t* page_table,
                    int32_t max_pages, const int32_t* cache_lens) {
   if (n_pages <= 0 || n_pages > INT32_MAX || page_size <= 0 || max_pages <= 0) return KDA_ERR_SHAPE;
-  if ((int64_t)max_pages * page_size > (int64_t)INT32_MAX) return KDA_ERR_SHAPE;
+  if ((int64_t)max_pages * page_size > (int64_t)1 << 30) return KDA_ERR_SHAPE;   // (32-bit positions, and a tile's room)
   if (!cache || !page_table || !cache_lens) return KDA_ERR_NULL;
   if (!aligned16(cache) || !aligned4(page_table) || !aligned4(cache_lens)) return KDA_ERR_ALIGN;
   return KDA_OK;

@@ -28,7 +28,7 @@
 // per state: with 256 threads it took 223 us). A state comes into shared memory by four TMA boxes
 // of 32 columns with 128-byte swizzle: the k index of a product's step runs over eight rows as 0
 // 2 4 6 | 1 3 5 7, which makes the fragments' reads free of bank conflicts. The next state's
-// inputs come through registers meanwhile. 256 x 32 states, 8 tokens: 164 us, 3.8 TB/s, 0.59 of
+// inputs come through registers meanwhile. 256 x 32 states, 8 tokens: 157 us, 4.0 TB/s, 0.61 of
 // the measured copy rate; issue is 59 % busy and the barriers between a state's steps come next.
 #pragma once
 
@@ -87,6 +87,14 @@ __device__ __forceinline__ void split_tf32(float a, uint32_t& a1, uint32_t& a2) 
 __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Four 8x8 b16 matrices from the rows that threads 8m .. 8m+7 address: matrix m to register m, row
+// t / 4, columns 2(t % 4) and one further.
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 // Warp-level bf16 MMA m16n8k16 (fp32 accumulate). Fragments (g = lane / 4, t = lane % 4), pairs of k:
 //   A 16x16: a0 = A[g][2t..], a1 = A[g+8][2t..], a2 = A[g][2t+8..], a3 = A[g+8][2t+8..]
@@ -224,13 +232,8 @@ kda_decode_tree_kernel(const __grid_constant__ CUtensorMap map_s, const TQ* __re
     // the rows for the product: e^G of the decay summed along the token's path
     for (int r = tid >> 7; r < n_tokens; r += TREE_THREADS / D) {
       const int c = tid & (D - 1);
-      const uint32_t anc = (uint32_t)s_anc[r];
       float g = 0.f;
-#pragma unroll 4
-      for (int i = 0; i <= r; ++i) {
-        const float l = s_g[i * D + c];
-        if ((anc >> i) & 1u) g += l;
-      }
+      for (int i = r; i >= 0; i = s_par[i]) g += s_g[i * D + c];
       const float e = exp2f(g);
       const float xk = s_k[r * D + c] * e, xq = s_q[r * D + c] * e;
       const int ak = r * TREE_XS + c, aq = (8 * MT + r) * TREE_XS + c;
@@ -303,8 +306,10 @@ kda_decode_tree_kernel(const __grid_constant__ CUtensorMap map_s, const TQ* __re
         return *reinterpret_cast<const float*>((odd ? s_odd : s_even) + eight * 1024);
       };
       if constexpr (BF) {
-        const __nv_bfloat16* x1 = s_x1 + g8 * TREE_XS + 2 * t4;
-        const __nv_bfloat16* x2 = s_x2 + g8 * TREE_XS + 2 * t4;
+        // (thread l gives the address of row l % 16 of a fragment's 16 x 16 block, its left or
+        // right half)
+        const uint32_t x1 = smem_u32(s_x1 + (lane & 15) * TREE_XS + 8 * (lane >> 4));
+        const uint32_t x2 = smem_u32(s_x2 + (lane & 15) * TREE_XS + 8 * (lane >> 4));
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           uint32_t b1[2], b2[2];
@@ -317,12 +322,8 @@ kda_decode_tree_kernel(const __grid_constant__ CUtensorMap map_s, const TQ* __re
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             uint32_t a1[4], a2[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {   // rows g8, g8 + 8; k 2t, 2t+1 of the first and the second eight
-              const int at = (16 * m + 8 * (i & 1)) * TREE_XS + 16 * ks + 8 * (i >> 1);
-              a1[i] = *reinterpret_cast<const uint32_t*>(x1 + at);
-              a2[i] = *reinterpret_cast<const uint32_t*>(x2 + at);
-            }
+            ldmatrix_x4(x1 + (uint32_t)((16 * m * TREE_XS + 16 * ks) * sizeof(__nv_bfloat16)), a1);
+            ldmatrix_x4(x2 + (uint32_t)((16 * m * TREE_XS + 16 * ks) * sizeof(__nv_bfloat16)), a2);
             mma_bf16_16x8x16(sml[m], a2, b1);
             mma_bf16_16x8x16(sm2[m], a1, b2);
             mma_bf16_16x8x16(acc[m], a1, b1);

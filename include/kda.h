@@ -430,6 +430,7 @@ int kda_decode_tree(const void* q, const void* k, const void* v, const void* log
  *
  * The cache is paged: cache [n_pages, page_size, 576] bf16; row p of sequence n lies in page
  * page_table[n][p / page_size], at row p % page_size. page_table is [n_seqs, max_pages] int32
+ * (max_pages * page_size at most 2^30 rows)
  * and cache_lens [n_seqs] int32, both on the device and read when the kernels run. cache_lens[n]
  * counts the sequence's rows WITH its new tokens, in every call: append the new tokens, then
  * attend, with the same array. Rows at and past cache_lens[n] are never used, whatever they

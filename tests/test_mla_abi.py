@@ -99,7 +99,7 @@ def test_decode_validation(lib):
         assert f(**{p: FAKE + 2}) == _native.KDA_ERR_ALIGN
     for bad in (dict(n=0), dict(t=0), dict(t=_native.KDA_DECODE_MAX_TOKENS + 1), dict(H=0),
                 dict(n=1 << 20, t=16, H=1 << 8), dict(page=0), dict(page=12), dict(pages=0),
-                dict(pages=1 << 31), dict(most=0), dict(most=1 << 26), dict(scale=0.0),
+                dict(pages=1 << 31), dict(most=0), dict(most=(1 << 24) + 1), dict(scale=0.0),
                 dict(scale=float("nan"))):
         assert f(**bad) == _native.KDA_ERR_SHAPE
 
