@@ -452,8 +452,9 @@ def mla_append(x, norm_w, cache, page_table, cache_lens, cu_seqlens=None, latent
         _need(latent, "latent", torch.bfloat16, (T, MLA_LATENT), dev)
     elif output_latent:
         latent = torch.empty((T, MLA_LATENT), dtype=torch.bfloat16, device=dev)
-    _launch(lib.kda_mla_append, "kda_mla_append", dev, *xs, _ptr(norm_w), float(eps), _ptr(cache), n_pages, page_size, _ptr(page_table), max_pages,
-            _ptr(cache_lens), _ptr(cu_seqlens), N, T, _ptr(latent))
+    _launch(lib.kda_mla_append, "kda_mla_append", dev, *xs, _ptr(norm_w), float(eps), _ptr(cache),
+            n_pages, page_size, _ptr(page_table), max_pages, _ptr(cache_lens), _ptr(cu_seqlens), N,
+            T, _ptr(latent))
     return latent
 
 

@@ -130,7 +130,7 @@ kda_mla_append_kernel(const __nv_bfloat16* __restrict__ x, int64_t x_stride,
       dst[32 + lane] = b;
       if (lane < 8) dst[64 + lane] = c;
     }
-    if (latent) {
+    if (latent && ok) {   // (rows of no sequence are left as they are)
       uint4* dst = reinterpret_cast<uint4*>(latent + t * LATENT);
       dst[lane] = a;
       dst[32 + lane] = b;

@@ -430,13 +430,13 @@ int kda_decode_tree(const void* q, const void* k, const void* v, const void* log
  *
  * The cache is paged: cache [n_pages, page_size, 576] bf16; row p of sequence n lies in page
  * page_table[n][p / page_size], at row p % page_size. page_table is [n_seqs, max_pages] int32
- * (max_pages * page_size at most 2^30 rows)
- * and cache_lens [n_seqs] int32, both on the device and read when the kernels run. cache_lens[n]
- * counts the sequence's rows WITH its new tokens, in every call: append the new tokens, then
- * attend, with the same array. Rows at and past cache_lens[n] are never used, whatever they
- * hold; values before it must be finite. A page number outside [0, n_pages), or a length past
- * max_pages * page_size, is kept in bounds and flagged (KDA_ERR_PAGE from kda_device_status).
- * int32 arrays of these calls need 4-byte alignment only.
+ * (max_pages * page_size at most 2^30 rows) and cache_lens [n_seqs] int32, both on the device
+ * and read when the kernels run. cache_lens[n] counts the sequence's rows WITH its new tokens,
+ * in every call: append the new tokens, then attend, with the same array. Rows at and past
+ * cache_lens[n] are never used, whatever they hold; values before it must be finite. A page
+ * number outside [0, n_pages), or a length past max_pages * page_size, is kept in bounds and
+ * flagged (KDA_ERR_PAGE from kda_device_status). int32 arrays of these calls need 4-byte
+ * alignment only.
  */
 #define KDA_MLA_LATENT 512
 #define KDA_MLA_SHARED 64
@@ -458,7 +458,8 @@ int kda_decode_tree(const void* q, const void* k, const void* v, const void* log
  *               written and flagged.
  *   latent      [t_total, 512] bf16 output of the normalised latents (the expanded form's
  *               projection reads them), or NULL
- * Two tokens of one call must not share a row. Returns KDA_OK or a negative kda_status.
+ * Two tokens of one call must not share a row. A token of no sequence (behind the last one) is
+ * written nowhere and flagged (KDA_ERR_SEQLENS). Returns KDA_OK or a negative kda_status.
  */
 int kda_mla_append(const void* x, int64_t x_stride, const float* norm_w, float eps, void* cache,
                    int64_t n_pages, int32_t page_size, const int32_t* page_table,
@@ -522,9 +523,9 @@ int kda_mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const
  *   o        [n_seqs, n_tokens, n_heads, 512] bf16 output
  *   lse      [n_seqs, n_tokens, n_heads] fp32 output (natural logarithm), or NULL
  *   workspace, workspace_bytes   kda_mla_decode_workspace_size(n_tokens, n_heads) bytes on the
- *            current device, 16-byte aligned (KDA_ERR_SCRATCH if less). Nothing in it has to be set; it must
- *            stay untouched until the stream has passed the call: calls that may overlap on the
- *            GPU need one each.
+ *            current device, 16-byte aligned (KDA_ERR_SCRATCH if less). Nothing in it has to be
+ *            set; it must stay untouched until the stream has passed the call: calls that may
+ *            overlap on the GPU need one each.
  * Results do not depend on timing: the parts of a sequence are joined in a fixed order.
  * Precision: as kda_mla_prefill. Returns KDA_OK or a negative kda_status.
  */

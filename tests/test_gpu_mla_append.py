@@ -159,3 +159,18 @@ def test_large_offsets(kda):
     kda.mla_append(x, None, cache, table, torch.tensor([128, 2], dtype=torch.int32, device="cuda"))
     assert torch.equal(cache[-1, 126:], x[:2]) and torch.equal(cache[-2, :2], x[2:])
     assert int((cache != 0).any(-1).sum()) == 4
+
+
+def test_rows_behind_the_last_sequence_are_left(kda):
+    """A batch padded behind its last sequence: the padding (NaN here) is written nowhere, the
+    latent output's rows there stay, and the device reports the lengths."""
+    from channel_wise_gated_b200 import _native
+    new, lens, page = [3, 5], [20, 5], 16
+    s = setup(new, lens, page, seed=8)
+    a, b = s["cache"].clone(), s["cache"].clone()
+    want = kda.mla_append(s["x"], s["w"], a, s["table"], s["lens"], cu_seqlens=s["cu"], output_latent=True)
+    x = torch.cat([s["x"], torch.full((4, W), float("nan"), device="cuda").bfloat16()])
+    lat = torch.full((12, ref.LATENT), 7.0, device="cuda").bfloat16()
+    kda.mla_append(x, s["w"], b, s["table"], s["lens"], cu_seqlens=s["cu"], latent=lat)
+    assert kda.device_status() == _native.KDA_ERR_SEQLENS
+    assert torch.equal(a, b) and torch.equal(lat[:8], want) and bool((lat[8:] == 7).all())

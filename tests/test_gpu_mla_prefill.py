@@ -208,3 +208,19 @@ def test_bad_cu_seqlens_stay_in_bounds(kda):
     for bad in ([0, 60, 50, 100], [0, 40, 300, 100], [5, 40, 60, 90], [0, -7, 60, 100]):
         kda.mla_prefill(q, k, ks, v, cu_seqlens=i32(bad))
         assert kda.device_status() == _native.KDA_ERR_SEQLENS
+
+
+@pytest.mark.parametrize("n_seqs", [2, 40])
+def test_rows_behind_the_last_sequence_are_left(kda, n_seqs):
+    """A batch padded behind its last sequence: outputs there stay, the device reports it."""
+    from channel_wise_gated_b200 import _native
+    cu = [9 * n for n in range(n_seqs + 1)]
+    real, total = cu[-1], cu[-1] + 21
+    q, k, ks, v = draw(total, total, 2, 73)
+    want, lw = kda.mla_prefill(q[:real], k[:real], ks[:real], v[:real], cu_seqlens=i32(cu), output_lse=True)
+    out = torch.full((total, 2, 128), 7.0, device="cuda").bfloat16()
+    lse = torch.full((total, 2), 7.0, device="cuda")
+    kda.mla_prefill(q, k, ks, v, cu_seqlens=i32(cu), o=out, lse=lse)
+    assert kda.device_status() == _native.KDA_ERR_SEQLENS
+    assert torch.equal(out[:real], want) and torch.equal(lse[:real], lw)
+    assert bool((out[real:] == 7).all()) and bool((lse[real:] == 7).all())
