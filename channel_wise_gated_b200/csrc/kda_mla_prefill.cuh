@@ -473,6 +473,7 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
         weights(s, sc, reference(), t_s, sum);
         if (move_to(row_max(s))) {
           sum = make_float2(0.f, 0.f);
+          tmem_st_wait();   // (stores have no order among themselves: the first weights land before these)
           weights(s, sc, reference(), t_s, sum);
         }
       }
