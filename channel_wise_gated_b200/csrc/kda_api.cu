@@ -85,6 +85,31 @@ int chunk_simt_dispatch(const void* q, const void* k, const void* v, const float
                                                       n_seqs, t_total, n_heads, o, hT, stream);
 }
 
+typedef CUresult (*CtxGetCurrentFn)(CUcontext*);
+CtxGetCurrentFn ctx_get_current() {
+  static CtxGetCurrentFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<CtxGetCurrentFn>(p);
+  });
+  return fn;
+}
+
+// The driver call below works in the calling thread's current context. A host thread that has made
+// no runtime call yet has none, and its call would fail: the current device's primary context is
+// made current then, as the runtime's own calls do.
+bool context_current() {
+  CtxGetCurrentFn get_ctx = ctx_get_current();
+  CUcontext ctx = nullptr;
+  if (get_ctx != nullptr && get_ctx(&ctx) == CUDA_SUCCESS && ctx != nullptr) return true;
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+}
+
 // ---- tensor-core chunk kernel: TMA descriptors and launch ----
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -102,7 +127,7 @@ EncodeTiledFn tensor_map_encoder() {
         q == cudaDriverEntryPointSuccess)
       fn = reinterpret_cast<EncodeTiledFn>(p);
   });
-  return fn;
+  return context_current() ? fn : nullptr;
 }
 
 // 2-D view [rows][cols] of a token-major tensor, box [box_r][box_c].
@@ -425,20 +450,6 @@ int validate_cache(const void* cache, int64_t n_pages, int32_t page_size, const 
 // array's name only stands in for the symbol, so the address is looked up once per
 // device, with that device current, and kept together with the context it belongs
 // to: a new context on the same device (after cudaDeviceReset, say) looks it up again.
-typedef CUresult (*CtxGetCurrentFn)(CUcontext*);
-CtxGetCurrentFn ctx_get_current() {
-  static CtxGetCurrentFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<CtxGetCurrentFn>(p);
-  });
-  return fn;
-}
-
 constexpr int MAX_STATIC_DEVICES = 64;
 std::mutex g_static_mu;
 void* g_static_addr[MAX_STATIC_DEVICES] = {};
