@@ -417,11 +417,14 @@ cudaError_t launch_decode_tree_as(const CUtensorMap& map_s, const TQ* q, const T
                                   const TG* log_alpha, const TG* beta, const int32_t* tree, TQ* o, int n_tokens,
                                   int n_heads, int chains, int sms, int smem_sm, int reserved,
                                   cudaStream_t stream) {
-  const size_t smem = tree_smem_bytes(n_tokens, sizeof(TQ));
+  // (The attribute belongs to the kernel, not to the call: every call sets the same value, the most
+  // that any of them needs, so that calls from several host threads do not undo one another's.)
   const cudaError_t e = cudaFuncSetAttribute(kda_decode_tree_kernel<TQ, TG, MAXT>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)tree_smem_bytes(MAXT, sizeof(TQ)));
   if (e != cudaSuccess) return e;
-  // (one CTA per SM where two do not fit: fp32 inputs past 13 tokens)
+  const size_t smem = tree_smem_bytes(n_tokens, sizeof(TQ));
+  // (one CTA per SM where two do not fit: fp32 inputs past 14 tokens)
   const int per_sm = 2 * (smem + (size_t)reserved) <= (size_t)smem_sm ? 2 : 1;
   const int grid = chains < per_sm * sms ? chains : per_sm * sms;
   kda_decode_tree_kernel<TQ, TG, MAXT><<<(unsigned)grid, TREE_THREADS, smem, stream>>>(
