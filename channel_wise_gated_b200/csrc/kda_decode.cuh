@@ -378,10 +378,12 @@ template <typename TQ, typename TG, bool PF>
 cudaError_t launch_decode_tokens_as(const TQ* q, const TQ* k, const TQ* v, const TG* log_alpha,
                                     const TG* beta, float* state, TQ* o, int n_tokens,
                                     int n_heads, int chains, int sms, cudaStream_t stream) {
-  const size_t smem = dec_tokens_smem_bytes(n_tokens, sizeof(TQ), sizeof(TG), PF);
-  cudaError_t e = cudaFuncSetAttribute(kda_decode_tokens_kernel<TQ, TG, PF>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // (The attribute belongs to the kernel, not to the call: every call sets the same value, the most
+  // that any of them needs, so that calls from several host threads do not undo one another's.)
+  cudaError_t e = cudaFuncSetAttribute(kda_decode_tokens_kernel<TQ, TG, PF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)dec_tokens_smem_bytes(DEC_MAX_TOKENS, sizeof(TQ), sizeof(TG), PF));
   if (e != cudaSuccess) return e;
+  const size_t smem = dec_tokens_smem_bytes(n_tokens, sizeof(TQ), sizeof(TG), PF);
   const int grid = chains < 2 * sms ? chains : 2 * sms;
   kda_decode_tokens_kernel<TQ, TG, PF><<<grid, DEC_THREADS, smem, stream>>>(
       q, k, v, log_alpha, beta, state, o, n_heads, n_tokens, chains);

@@ -123,3 +123,24 @@ def test_trees_of_several_sizes_at_once(kda, tokens, dtype):
     assert run_at_once(lib.kda_decode_tree, args, 10000) == []
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
     assert kda.device_status() == 0
+
+@pytest.mark.parametrize("tokens", [(1, 2, 1, 2), (3, 8, 4, 7), (12, 16, 13, 15)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_token_runs_of_several_sizes_at_once(kda, tokens, dtype):
+    from channel_wise_gated_b200 import _native
+    lib, args, outs, want, keep = _native.load(), [], [], [], []
+    kind = _native.KDA_BF16 if dtype == torch.bfloat16 else _native.KDA_F32
+    for t in tokens:
+        d = kda_inputs.make_decode(1, 2, t, dtype, dtype, seed=420 + t, device="cuda")
+        x = [d[n].transpose(0, 1).contiguous() for n in ("q", "k", "v", "log_alpha", "beta")]
+        x[3].zero_()
+        x[4].zero_()     # no decay, beta 0: the state stays as it is over the calls
+        want.append(kda.decode_tokens(*x, d["state"].clone()))
+        outs.append(torch.zeros_like(want[-1]))
+        stream = torch.cuda.Stream()
+        keep.append((x, d, stream))
+        args.append([y.data_ptr() for y in x] + [d["state"].data_ptr(), outs[-1].data_ptr(), 1, t, 2, kind, kind,
+                                                 stream.cuda_stream])
+    assert run_at_once(lib.kda_decode_tokens, args, 10000) == []
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert kda.device_status() == 0
