@@ -52,17 +52,30 @@ __device__ __forceinline__ float sumsq8(uint4 v, float by) {
   }
   return s;
 }
-__device__ __forceinline__ uint4 scale8(uint4 v, float r, const float (&w)[8]) {
+// eight bf16 values times `by` (a power of two), r and their weights
+__device__ __forceinline__ uint4 scale8(uint4 v, float by, float r, const float (&w)[8]) {
   uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float a = __uint_as_float(u[i] << 16) * r * w[2 * i];
-    const float b = __uint_as_float(u[i] & 0xFFFF0000u) * r * w[2 * i + 1];
+    const float a = __uint_as_float(u[i] << 16) * by * r * w[2 * i];
+    const float b = __uint_as_float(u[i] & 0xFFFF0000u) * by * r * w[2 * i + 1];
     const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
     u[i] = *reinterpret_cast<const uint32_t*>(&p);
   }
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
+__device__ __forceinline__ float warp_sum(float s) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  return s;
+}
+// Rows whose squares leave fp32: at 2^80 or 2^-70 of their size, where they do not. Below 2^-100 a
+// sum of squares loses bits to subnormals (up to 2^-150 of it per product), which counts unless
+// eps is above 2^-120; past 2^128 it is infinite (bf16 holds values from 2^-133 to 2^128).
+constexpr float SUM_LEAST = 7.888609052210118e-31f;    // 2^-100
+constexpr float EPS_LEAST = 7.52316384526264e-37f;     // 2^-120
+constexpr float BY_SMALL = 1.2089258196146292e24f;     // 2^80
+constexpr float BY_LARGE = 8.470329472543003e-22f;     // 2^-70
 
 __global__ void __launch_bounds__(APPEND_THREADS)
 kda_mla_append_kernel(const __nv_bfloat16* __restrict__ x, int64_t x_stride,
@@ -108,21 +121,18 @@ kda_mla_append_kernel(const __nv_bfloat16* __restrict__ x, int64_t x_stride,
       }
     }
     if (norm_w) {
-      float s = sumsq8(a, 1.f) + sumsq8(b, 1.f);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      float r = 1.f / sqrtf(s * (1.f / LATENT) + eps);
-      if (!(s < INFINITY)) {
-        // values past 8e17, whose squares' sum leaves fp32 (bf16 holds up to 3.4e38): once
-        // more at 2^-70 of the size, where eps no longer counts
-        constexpr float SMALL = 8.470329472543003e-22f;
-        s = sumsq8(a, SMALL) + sumsq8(b, SMALL);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        r = SMALL / sqrtf(s * (1.f / LATENT));
+      float s = warp_sum(sumsq8(a, 1.f) + sumsq8(b, 1.f));
+      if (s < INFINITY && (s >= SUM_LEAST || eps >= EPS_LEAST)) {
+        const float r = 1.f / sqrtf(s * (1.f / LATENT) + eps);
+        a = scale8(a, 1.f, r, w0);
+        b = scale8(b, 1.f, r, w1);
+      } else {
+        const float by = s < INFINITY ? BY_SMALL : BY_LARGE;   // (2^160 eps stays below 2^40)
+        s = warp_sum(sumsq8(a, by) + sumsq8(b, by));
+        const float r = 1.f / sqrtf(fmaf(eps * by, by, s * (1.f / LATENT)));
+        a = scale8(a, by, r, w0);
+        b = scale8(b, by, r, w1);
       }
-      a = scale8(a, r, w0);
-      b = scale8(b, r, w1);
     }
     if (page >= 0) {
       uint4* dst = reinterpret_cast<uint4*>(cache + ((int64_t)page * page_size + pos % page_size) * WIDTH);

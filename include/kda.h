@@ -450,7 +450,8 @@ int kda_decode_tree(const void* q, const void* k, const void* v, const void* log
  *   x           [t_total, 576] bf16, rows x_stride elements apart (a multiple of 8, at least
  *               576: x may be a slice of a wider projection output)
  *   norm_w      [512] fp32, or NULL: the latents are cached as they are
- *   eps         >= 0
+ *   eps         >= 0. Rows whose squares leave fp32 at either end are normalised all the same; a
+ *               row of zeros with eps = 0 gives NaN (0 / 0)
  *   cu_seqlens  [n_seqs + 1] int32 as kda_chunk_fwd (sequence n's new tokens), or NULL: n_seqs
  *               equal runs of t_total / n_seqs tokens
  *   cache_lens  lengths after the append: token i of the T_n new ones of sequence n is row
