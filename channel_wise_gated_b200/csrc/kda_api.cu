@@ -870,7 +870,8 @@ int kda_mla_decode(const void* q, const void* cache, int64_t n_pages, int32_t pa
   using namespace kda::mla;
   using namespace kda::mla::dec;
   if (n_seqs <= 0 || n_heads <= 0 || n_tokens <= 0 || n_tokens > KDA_DECODE_MAX_TOKENS ||
-      (int64_t)n_seqs * n_tokens * n_heads > (int64_t)INT32_MAX - 64 || !(scale > 0.f && scale < 1e30f))
+      (int64_t)n_seqs > ((int64_t)INT32_MAX - 64) / ((int64_t)n_tokens * n_heads) ||   // (the product could leave 64 bits)
+      !(scale > 0.f && scale < 1e30f))
     return KDA_ERR_SHAPE;
   const int st = validate_cache(cache, n_pages, page_size, page_table, max_pages, cache_lens);
   if (st != KDA_OK) return st;
