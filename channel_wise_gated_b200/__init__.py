@@ -357,7 +357,9 @@ def decode_tree(q, k, v, log_alpha, beta, state, tree=None, o=None):
     [N, t, H] (bf16 or fp32, same dtype); state: [N, H, 128, 128] fp32; tree: [N, t] int32,
     bit i of tree[n, r] set if token i is an ancestor of token r or r itself, parents before
     their children (None: a chain). Token r's output is the recurrence's after the tokens of
-    its path. Returns o like q. The accepted path is then applied with decode_tokens.
+    its path. With bf16 q, k, v the products with the state are taken in two bf16 parts of each
+    factor, off by at most 3 * 2^-16 of their terms' absolute sum; fp32 ones keep fp32's
+    accuracy. Returns o like q. The accepted path is then applied with decode_tokens.
     """
     lib = _native.load()
     if q.dim() != 4 or q.shape[3] != D:

@@ -20,9 +20,11 @@
 // instructions a warp and 267 us for 256 x 32 states and 8 tokens (FMA pipe 34 % busy, the rest
 // of the issue spent on pairing operands and summing over warps). So it runs on the warp-level
 // tensor cores with every fp32 operand split in two, a = a1 + a2, and a b = a1 b1 + a1 b2 + a2 b1.
-// For fp32 inputs the parts are tf32: what is left out is 2^-22 of a b, the accuracy of fp32
-// sums. For bf16 inputs they are bf16 (2^-16, against an output rounded by 2^-8), which halves the
-// products. A warp takes 8 columns and the whole depth, so no sums cross warps.
+// For fp32 inputs the parts are tf32: the products left out and the parts' own roundings are at most
+// 3 2^-22 of |a b|, the accuracy of fp32 sums. For bf16 inputs they are bf16, at most 3 2^-16 of |a b|
+// (of the state too, although that is fp32), against an output rounded by 2^-8 of its value: fewer
+// bits than decode_tokens keeps, which show where a sum cancels to 2^-8 of its terms. That halves
+// the products. A warp takes 8 columns and the whole depth, so no sums cross warps.
 //
 // Two persistent CTAs of 512 threads per SM walk the states (a chain of short dependent steps
 // per state: with 256 threads it took 223 us). A state comes into shared memory by four TMA boxes
@@ -78,7 +80,7 @@ __device__ __forceinline__ void piece_to_f32(uint4 raw, float* dst, float by = 1
   }
 }
 
-// a = a1 + a2 + (2^-22 a), both parts in tf32
+// a = a1 + a2 + (at most 2^-22 |a|), both parts in tf32
 __device__ __forceinline__ void split_tf32(float a, uint32_t& a1, uint32_t& a2) {
   a1 = sm100::f2tf32(a);
   a2 = sm100::f2tf32(a - __uint_as_float(a1));

@@ -403,8 +403,13 @@ int kda_decode_tokens(const void* q, const void* k, const void* v, const void* l
  *
  * Token r's output is what the recurrence gives after the tokens of its path, in order,
  * from the sequence's state:  S <- (I - beta k k^T) Diag(alpha) S + beta k v^T over the
- * path, o_r = S^T q_r. Computed in the chunk form (fp32) with "earlier token" replaced by
- * "ancestor", so a chain equals kda_decode_tokens in real arithmetic, not bit for bit.
+ * path, o_r = S^T q_r. Computed in the chunk form with "earlier token" replaced by "ancestor", so
+ * a chain equals kda_decode_tokens in real arithmetic, not bit for bit.
+ * Precision: fp32 sums throughout. The products of the decayed k and q rows x with the state take
+ * each factor as two parts: for fp32 q, k, v tf32 parts, off by at most 3 * 2^-22 of sum_c |x_c S_cj|,
+ * for bf16 ones bf16 parts, 3 * 2^-16 of it (also of an fp32 state: coarser than kda_decode_tokens,
+ * and more than the bf16 output's own rounding only where a sum cancels to under 2^-8 of its
+ * terms; pass fp32 q, k, v where that matters).
  *
  * Arguments: as kda_decode_tokens, but
  *   state   [n_seqs, n_heads, 128, 128] fp32, read only
