@@ -63,16 +63,20 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _launch(fn, where, dev, *args):
-    """Call an entry point on dev's current stream, with dev the current device. (A device guard
-    and a Stream object cost 3.6 us of a call's host time: the guard is taken only where it is
-    needed, the stream's handle read as it is.)"""
+def _call(fn, dev, *args) -> int:
+    """Call an entry point on dev's current stream, with dev the current device; its status. (A
+    device guard and a Stream object cost 3.6 us of a call's host time: the guard is taken only
+    where it is needed, the stream's handle read as it is.)"""
     stream = torch._C._cuda_getCurrentRawStream(dev.index)
     if torch.cuda.current_device() == dev.index:
-        st = fn(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, stream)
+        return fn(*args, stream)
+    with torch.cuda.device(dev):
+        return fn(*args, stream)
+
+
+def _launch(fn, where, dev, *args):
+    """_call, with a status other than KDA_OK raised."""
+    st = _call(fn, dev, *args)
     if st:
         _native.check(st, where)
 
@@ -568,7 +572,10 @@ def mla_decode(q, cache, page_table, cache_lens, tree=None, scale=None, o=None, 
 
 
 def device_status(device=None) -> int:
-    """Read and clear the library's device-side error word (synchronises)."""
+    """Read and clear the library's error word on the device (default: the current one);
+    synchronises that device's current stream."""
     lib = _native.load()
     dev = torch.device("cuda") if device is None else torch.device(device)
-    return int(lib.kda_device_status(_stream_ptr(dev)))
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    return int(_call(lib.kda_device_status, dev))
