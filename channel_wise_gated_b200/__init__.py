@@ -37,10 +37,6 @@ PREFILL_COMPUTE_DTYPE = "bf16"
 _DT = {torch.float32: _native.KDA_F32, torch.bfloat16: _native.KDA_BF16}
 
 
-def _stream_ptr(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
-
-
 def _need(t: torch.Tensor, name: str, dtype=None, shape=None, device=None):
     if (shape is not None and device is not None and isinstance(t, torch.Tensor) and t.is_cuda
             and t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()):
@@ -131,9 +127,8 @@ def dplr_chunk_fwd(q, k, v, a, b, log_alpha, h0=None, cu_seqlens=None, o=None, h
     args, (o, hT, N, T, H) = _prefill_args(q, k, v, log_alpha, (D,), dummy_beta, h0, cu_seqlens,
                                            o, hT, output_final_state)
     q_, k_, v_, la_, _, h0_, cu_, N_, T_, H_, dt_, o_, hT_ = args
-    st = lib.kda_dplr_chunk_fwd(q_, k_, v_, _ptr(a), _ptr(b), la_, h0_, cu_, N_, T_, H_, dt_, o_,
-                                hT_, _stream_ptr(q.device))
-    _native.check(st, "kda_dplr_chunk_fwd")
+    _launch(lib.kda_dplr_chunk_fwd, "kda_dplr_chunk_fwd", q.device, q_, k_, v_, _ptr(a), _ptr(b),
+            la_, h0_, cu_, N_, T_, H_, dt_, o_, hT_)
     return o, hT
 
 
@@ -158,9 +153,8 @@ def short_conv_swish(x, w, cu_seqlens=None, y=None):
         y = torch.empty_like(x)
     else:
         _need(y, "y", torch.bfloat16, tuple(x.shape), dev)
-    st = lib.kda_short_conv_swish(_ptr(x), _ptr(w), _ptr(cu_seqlens), N, T, C, _ptr(y),
-                                  _stream_ptr(dev))
-    _native.check(st, "kda_short_conv_swish")
+    _launch(lib.kda_short_conv_swish, "kda_short_conv_swish", dev, _ptr(x), _ptr(w),
+            _ptr(cu_seqlens), N, T, C, _ptr(y))
     return y
 
 
@@ -190,9 +184,8 @@ def chunk_fwd_fused(q_pre, k_pre, v, decay_pre, beta_pre, gate_pre, norm_w, h0=N
                                                     int(cu_seqlens is not None))
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
     q_, k_, v_, _, b_, h0_, cu_, N_, T_, H_, _, o_, hT_ = args
-    st = lib.kda_chunk_fwd_fused(q_, k_, v_, _ptr(decay_pre), b_, _ptr(gate_pre), _ptr(norm_w),
-                                 h0_, cu_, N_, T_, H_, o_, hT_, _ptr(ws), ws_bytes, _stream_ptr(dev))
-    _native.check(st, "kda_chunk_fwd_fused")
+    _launch(lib.kda_chunk_fwd_fused, "kda_chunk_fwd_fused", dev, q_, k_, v_, _ptr(decay_pre), b_,
+            _ptr(gate_pre), _ptr(norm_w), h0_, cu_, N_, T_, H_, o_, hT_, _ptr(ws), ws_bytes)
     return o, hT
 
 
@@ -212,8 +205,7 @@ def gdn_chunk_fwd(q, k, v, log_a, beta, h0=None, cu_seqlens=None, o=None, hT=Non
         ws_bytes = lib.kda_chunk_fwd_workspace_size(N, T, H, _DT[q.dtype],
                                                     int(cu_seqlens is not None))
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device) if ws_bytes else None
-    st = lib.kda_gdn_chunk_fwd_ws(*args, _ptr(ws), ws_bytes, _stream_ptr(q.device))
-    _native.check(st, "kda_gdn_chunk_fwd_ws")
+    _launch(lib.kda_gdn_chunk_fwd_ws, "kda_gdn_chunk_fwd_ws", q.device, *args, _ptr(ws), ws_bytes)
     return o, hT
 
 
@@ -264,19 +256,17 @@ def chunk_fwd(q, k, v, log_alpha, beta, h0=None, cu_seqlens=None, o=None, hT=Non
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(h0), _ptr(cu_seqlens),
             N, T, H, _DT[q.dtype], _ptr(o), _ptr(hT))
     if kernel == "simt":
-        st, name = lib.kda_chunk_fwd_simt(*args, _stream_ptr(dev)), "kda_chunk_fwd_simt"
+        _launch(lib.kda_chunk_fwd_simt, "kda_chunk_fwd_simt", dev, *args)
     elif kernel == "static":
-        st, name = lib.kda_chunk_fwd_static(*args, _stream_ptr(dev)), "kda_chunk_fwd_static"
+        _launch(lib.kda_chunk_fwd_static, "kda_chunk_fwd_static", dev, *args)
     else:
         ws_bytes = 0
         if kernel == "auto":
             ws_bytes = lib.kda_chunk_fwd_workspace_size(N, T, H, _DT[q.dtype],
                                                         int(cu_seqlens is not None))
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
-        st = lib.kda_chunk_fwd_ws(*args, _ptr(ws), ws_bytes, _stream_ptr(dev))
-        name = "kda_chunk_fwd_ws"
+        _launch(lib.kda_chunk_fwd_ws, "kda_chunk_fwd_ws", dev, *args, _ptr(ws), ws_bytes)
         # (the caching allocator keeps ws alive for the stream's use of it)
-    _native.check(st, name)
     return o, hT
 
 
@@ -316,9 +306,9 @@ def decode_step(q, k, v, log_alpha, beta, state, o=None):
         o = torch.empty_like(q)
     else:
         _need(o, "o", q.dtype, (N, H, D), dev)
-    st = lib.kda_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(state),
-                             _ptr(o), N, H, _DT[q.dtype], _DT[log_alpha.dtype], _stream_ptr(dev))
-    _native.check(st, "kda_decode_step")
+    _launch(lib.kda_decode_step, "kda_decode_step", dev, _ptr(q), _ptr(k), _ptr(v),
+            _ptr(log_alpha), _ptr(beta), _ptr(state), _ptr(o), N, H, _DT[q.dtype],
+            _DT[log_alpha.dtype])
     return o
 
 
@@ -347,10 +337,9 @@ def decode_tokens(q, k, v, log_alpha, beta, state, o=None):
         o = torch.empty_like(q)
     else:
         _need(o, "o", q.dtype, (N, t, H, D), dev)
-    st = lib.kda_decode_tokens(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta),
-                               _ptr(state), _ptr(o), N, t, H, _DT[q.dtype], _DT[log_alpha.dtype],
-                               _stream_ptr(dev))
-    _native.check(st, "kda_decode_tokens")
+    _launch(lib.kda_decode_tokens, "kda_decode_tokens", dev, _ptr(q), _ptr(k), _ptr(v),
+            _ptr(log_alpha), _ptr(beta), _ptr(state), _ptr(o), N, t, H, _DT[q.dtype],
+            _DT[log_alpha.dtype])
     return o
 
 

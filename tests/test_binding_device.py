@@ -86,3 +86,25 @@ NEW = {
 def test_calls_run_on_their_tensors_device(gpu, name):
     NEW[name]()
     assert gpu.calls == [(name, 1, 1007)] and gpu.current == 0
+
+
+C = (t(70, 2, 128), t(70, 2, 128), t(70, 2, 128), t(70, 2, 128, dtype=F32), t(70, 2, dtype=F32))
+OUT = dict(o=t(70, 2, 128), hT=t(1, 2, 128, 128, dtype=F32))
+KDA = {
+    "kda_chunk_fwd_ws": lambda: kda.chunk_fwd(*C, **OUT),
+    "kda_chunk_fwd_simt": lambda: kda.chunk_fwd(*C, **OUT, kernel="simt"),
+    "kda_chunk_fwd_static": lambda: kda.chunk_fwd(*C, **OUT, kernel="static"),
+    "kda_gdn_chunk_fwd_ws": lambda: kda.gdn_chunk_fwd(*C[:3], t(70, 2, dtype=F32), C[4], **OUT),
+    "kda_chunk_fwd_fused": lambda: kda.chunk_fwd_fused(*C[:3], C[0], C[4], C[0], t(128, dtype=F32), **OUT),
+    "kda_short_conv_swish": lambda: kda.short_conv_swish(t(5, 2, 128), t(256, 4, dtype=F32), y=t(5, 2, 128)),
+    "kda_decode_step": lambda: kda.decode_step(*[t(3, 2, 128)] * 4, t(3, 2), t(3, 2, 128, 128, dtype=F32),
+                                               o=t(3, 2, 128)),
+    "kda_decode_tokens": lambda: kda.decode_tokens(*[t(2, 3, 2, 128)] * 4, t(2, 3, 2),
+                                                   t(2, 2, 128, 128, dtype=F32), o=t(2, 3, 2, 128)),
+}
+
+
+@pytest.mark.parametrize("name", KDA)
+def test_kda_calls_run_on_their_tensors_device(gpu, name):
+    KDA[name]()
+    assert gpu.calls == [(name, 1, 1007)] and gpu.current == 0
