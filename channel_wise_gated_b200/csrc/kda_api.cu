@@ -836,8 +836,8 @@ int kda_mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const
          encode_heads(&mv, v, kda::D, n_heads, tk_total, v_stride_t, v_stride_h, 64) &&
          encode_bf16(&ms, k_shared, 2, dims, strides, box);
   }
-  if (!ok || cudaFuncSetAttribute(kda_mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  (int)SMEM_BYTES) != cudaSuccess)
+  const auto kernel = tk_total > (int64_t)FOLD * BN ? kda_mla_prefill_kernel<true> : kda_mla_prefill_kernel<false>;
+  if (!ok || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES) != cudaSuccess)
     return KDA_ERR_CUDA;
   Args a;
   a.cu_q = cu_seqlens_q;
@@ -851,7 +851,7 @@ int kda_mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const
   a.lse = lse;
   a.scale = scale;
   a.causal = causal != 0;
-  kda_mla_prefill_kernel<<<(unsigned)(tiles * n_heads), THREADS, SMEM_BYTES, stream>>>(mq, mk, ms, mv, a);
+  kernel<<<(unsigned)(tiles * n_heads), THREADS, SMEM_BYTES, stream>>>(mq, mk, ms, mv, a);
   return launch_status();
 }
 

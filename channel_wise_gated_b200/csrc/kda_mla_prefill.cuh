@@ -98,6 +98,14 @@ constexpr int BM = 128;             // queries per tile
 constexpr int PAIR = 2 * BM;        // queries per CTA
 constexpr int LATE_START = 40;      // key tiles from which on tile B starts behind A
 constexpr int BN = 128;             // keys per tile
+// Key tiles after which a row's accumulators are taken out and begin anew, in calls that can have
+// more (PARTS): the matrix units cut each sum to fp32 instead of rounding it, and 65,536 of them
+// in a row (1,048,576 keys) lost 0.6 % of values of one sign, more than the output's rounding. 4,096
+// lose 0.05 % at most, and the parts are added with rounding. In every call it would cost 1 to 2 %
+// (190 against 188 us for 4,096 tokens and 32 heads, 1,253 against 1,226 for 32,768 and 4: the
+// loop's registers). Where a call has more keys: 64 prompts of 1,100 (none of them long), 8 heads 424
+// against 416 us; 1,024 tokens behind 130,048, 4 heads 2,252 against 2,405.
+constexpr int FOLD = 512;
 constexpr int THREADS = 384;
 constexpr uint32_t BLK = 128 * 128; // 16 KiB: a 128-row block of 64 bf16 columns
 constexpr uint32_t Q_BYTES = 3 * BLK;
@@ -230,6 +238,8 @@ __device__ __forceinline__ void weights(const float* s, float sc, float ms, uint
   sum = __fadd2_rn(sum, part);
 }
 
+// PARTS: some sequence may have more than FOLD key tiles
+template <bool PARTS>
 __global__ void __launch_bounds__(THREADS, 1)
 kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUtensorMap map_v,
@@ -424,6 +434,9 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
     const int see = a.causal ? min(len_k, row + off + 1) : len_k;   // keys this row sees
     const int n_x = nt[x];
     float m = -INFINITY, l = 0.f;
+    float kept[D + 1];   // (PARTS) accumulators taken out, and the reference they belong to: local memory
+    kept[D] = 0.f;
+    auto kept_by = [&]() { return kept[D] == m ? 1.f : exp2_fast((kept[D] - m) * sc); };
     bool alive = true;
     for (int j = 0; j < n_x; ++j) {
       if (!(alive = wait(&bars[B_SFULL + x], j & 1))) break;
@@ -443,20 +456,36 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
       // is found, and again in the rare tile that moves it. (The first tile, and a masked one,
       // find their maximum first.)
       float2 sum = make_float2(0.f, 0.f);
-      auto move_to = [&](float mt) {   // true for the warp if a row's reference moves
+      auto move_to = [&](float mt) {   // true for the warp if a row's reference moves, or the part ends
         const bool move = mt > m && (mt - m) * sc > RESCALE_LOG2;   // (from -inf: always)
-        if (!__any_sync(0xffffffffu, move)) return false;
+        const bool out = PARTS && j % FOLD == 0;
+        if (!__any_sync(0xffffffffu, move || out)) return false;
         // (P V of the tile before has completed: it was issued before the S waited for)
         const float f = move ? exp2_fast((m - mt) * sc) : 1.f;
         if (move) m = mt;
         l *= f;
-#pragma unroll
+        float kf = 0.f;
+        if constexpr (PARTS) {
+          if (out) {
+            kf = kept_by();
+            kept[D] = m;
+          }
+        }
+#pragma unroll (PARTS ? 1 : 8)
         for (int c = 0; c < 8; ++c) {
           float v[16];
           tmem_ld16(t_o + 16 * c, v);
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] *= f;
+          if constexpr (PARTS) {
+            if (out)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                kept[16 * c + i] = j == FOLD ? v[i] : fmaf(kept[16 * c + i], kf, v[i]);
+                v[i] = 0.f;
+              }
+          }
           tmem_st16(t_o + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&v));
         }
         return true;
@@ -500,6 +529,13 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
         if (n_x > 0) {
           tmem_ld32(t_o + 32 * c, v);
           tmem_ld_wait();
+        }
+        if constexpr (PARTS) {
+          if (n_x > FOLD) {
+            const float f = kept_by();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = fmaf(kept[32 * c + i], f, v[i]);
+          }
         }
         if (row < len_q) {
 #pragma unroll
