@@ -30,8 +30,8 @@
 // per state: with 256 threads it took 223 us). A state comes into shared memory by four TMA boxes
 // of 32 columns with 128-byte swizzle: the k index of a product's step runs over eight rows as 0
 // 2 4 6 | 1 3 5 7, which makes the fragments' reads free of bank conflicts. The next state's
-// inputs come through registers meanwhile. 256 x 32 states, 8 tokens: 157 us, 4.0 TB/s, 0.61 of
-// the measured copy rate; issue is 54 % busy, shared memory's pipe 61 %, the rest is barriers.
+// inputs come through registers meanwhile. 256 x 32 states, 8 tokens: 157 to 162 us, 3.8 to 4.0
+// TB/s, 0.59 to 0.61 of the measured copy rate; issue is 54 % busy, shared memory's pipe 61 %, the rest is barriers.
 #pragma once
 
 #include "kda_common.cuh"

@@ -6,9 +6,9 @@
 // Bound: 1,152 bytes read and 1,152 written per token (1,024 more with the latent output),
 // no reuse, so HBM for long batches and launch latency for a few tokens. One warp per token:
 // each lane takes two 16-byte pieces of the latent, the sum of squares is one warp reduction,
-// and the row is written as it was read, so every access is a full 512-byte line run. 89,191
-// tokens with the latent output: 41.2 us, 5.1 TB/s, 0.80 of the measured copy rate (more warps, or
-// the next row's loads ahead of the present row's work, were 8 to 20 % slower).
+// and the row is written as it was read, so every access is a full 512-byte line run. 63,657
+// tokens with the latent output (212 MB): 41.2 to 41.8 us, 5.1 TB/s, 0.79 of the measured copy rate
+// (more warps, or the next row's loads ahead of the present row's work, were 8 to 20 % slower).
 #pragma once
 
 #include "kda_common.cuh"

@@ -21,13 +21,15 @@
 // The work of all sequences is one line of tiles, cut into equal runs, one per CTA, so ragged
 // lengths and few long sequences fill the GPU alike. A run covers parts of one or more
 // (sequence, row group) items; an item cut by a run's border is left as partial sums (fp32) in
-// the workspace and joined by a second kernel in a fixed order.
+// the workspace and joined by a second kernel in a fixed order. The matrix units cut each sum to
+// fp32, twice a tile: a run of 131,072 rows of one sequence loses up to 0.1 % of values of one sign,
+// which takes 22 GB of cache in one call.
 //
-// Measured: 128 sequences of 1k to 8k rows, 32 heads, one token: 134 to 153 us by clock (721 MB; a
+// Measured: 128 sequences of 1k to 8k rows, 32 heads, one token: 134 to 154 us by clock (720 MB; a
 // read of them alone takes 121). Per tile of 32 keys S takes 36 products of 27 cycles (64 x 32 x
 // 16: the operands' reads, not the multiplications), P V 8 of 43 (32 rows) to 50 (64); copies of
 // the stages not held by products keep about 110 KiB in flight per SM. 48 trees of 8 tokens (256
-// rows a sequence, four items that share the cache in L2): 203 to 234 us, bound by S.
+// rows a sequence, four items that share the cache in L2): 203 to 237 us, bound by S.
 #pragma once
 
 #include "kda_common.cuh"
@@ -46,9 +48,11 @@ constexpr uint32_t GROUP = 8 * WIDTH * 2;               // 8 cached rows: nine 1
 constexpr uint32_t STAGE = BN / 8 * GROUP;              // 36,864 bytes
 constexpr int MAX_STAGES = 5;
 constexpr int LOOK = 4;                                 // tiles from reading a page's number to its copy
-// A CTA's run is at least this long: one sequence of 640 / 5,000 / 9,000 rows took 11.2 / 15.0 /
-// 20.4 us with 2 (more parts to join, and no idle SM for the join to start on), 12.1 / 14.8 / 17.6
-// with 3, 12.9 / 15.3 / 16.7 with 4.
+// A CTA's run is at least this long. One sequence of 640 / 5,003 / 9,001 rows, us with 2 (more parts to
+// join, and no idle SM for the join to start on), 3 and 4 tiles: 4 heads 9.9 / 13.4 / 16.5, 10.6 /
+// 13.3 / 15.2, 11.6 / 14.0 / 14.9; 32 heads 11.0 / 15.0 / 18.0, 11.6 / 14.6 / 17.4, 12.6 / 15.0 / 16.8;
+// 64 heads 12.5 / 17.6 / 20.9, 13.1 / 16.4 / 19.5, 14.2 / 16.9 / 18.9; 128 heads 13.1 / 18.4 / 19.9,
+// 13.9 / 20.7 / 19.9, 14.8 / 19.7 / 22.7. From 20,000 rows on they are the same.
 constexpr int MIN_TILES = 3;
 constexpr int MAX_GRID = 160;                           // CTAs of the main kernel at most (the join holds a part per lane and round)
 enum { B_KVFULL = 0, B_KVFREE = MAX_STAGES, B_SFULL = 2 * MAX_STAGES, B_PFULL = B_SFULL + 8, B_PVDONE = B_PFULL + 2,

@@ -19,11 +19,12 @@
 // bf16 and the accumulators need no pass of their own. Maxima, sums and O are fp32; P is rounded
 // to bf16 once (half a step, 2^-8 relative per weight) as the matrix units take it.
 //
-// Measured: 4,096 tokens, 32 heads in 171 us (1.0 PFLOP/s), 32,768 tokens, 4 heads in 1.21 ms
-// (1.14), 0.62 and 0.70 of the measured bf16 rate (0.72 and 0.81 of its sustained one). A pair of
-// key tiles takes about 4,100 cycles where its products need 2,680: both tiles' chains (S,
-// softmax of 2,000 cycles, P V) run nearly in step and wait for the special function unit and the
-// tensor cores in turn.
+// Measured, by clock: 4,096 tokens, 32 heads in 164 to 193 us (1.05 to 0.89 PFLOP/s), 32,768 tokens,
+// 4 heads in 1.15 to 1.25 ms (1.19 to 1.10): 0.64 to 0.54 and 0.73 to 0.67 of the measured bf16 rate
+// (0.85 to 0.78 of its sustained one for the latter). A pair of key tiles takes about 4,100 cycles
+// where its products need 2,680: both tiles' chains (S, softmax of 2,000 cycles, P V) run nearly in
+// step, so that the tensor cores and the softmax's units are busy half of the time each and
+// mostly not together.
 #pragma once
 
 #include "kda_common.cuh"
@@ -128,7 +129,7 @@ constexpr uint32_t IDESC_PV = sm100::idesc_bf16(128, 128, 0, 1);   // V is read 
 struct Args {
   const int32_t* cu_q;
   const int32_t* cu_k;
-  int n_seqs, n_heads, tiles;       // tiles: upper bound of the pairs of query tiles, all sequences
+  int n_seqs, n_heads;
   int64_t tq, tk;
   __nv_bfloat16* o;
   float* lse;
@@ -215,8 +216,8 @@ __device__ __forceinline__ float row_max(const float* s) {
 
 // Weights 2^(s sc - ms) of 64 scores, as bf16 pairs into tensor memory 16 registers at a time (32
 // made the loop spill, 2 to 3 % of its time), their sum added to `sum`. (Leaving every
-// fourth pair to a polynomial on the FMA units made 4,096 tokens slower, 238 against 221 us:
-// the special function unit is not what the softmax waits for.)
+// fourth pair to a polynomial on the FMA units made an early form of this kernel slower, 238 against
+// 221 us for 4,096 tokens; with the present order of work it has not been tried.)
 __device__ __forceinline__ void weights(const float* s, float sc, float ms, uint32_t t_p, float2& sum) {
   const float2 sc2 = make_float2(sc, sc), ms2 = make_float2(-ms, -ms);
   float2 part = make_float2(0.f, 0.f);
@@ -357,9 +358,11 @@ kda_mla_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
       const uint64_t q0 = make_sdesc(sb + OFF_Q + x * Q_BYTES, 16, 1024, SWZ_128B);
       bool alive = n_x == 0 || wait(&bars[B_QFULL + x], 0);
       // Over many tiles B starts when A's first weights are there, so that one tile's softmax falls
-      // into the other's products from then on: 1,255 against 1,320 us for 32,768 tokens and 4
-      // heads, 175 against 185 for 1,024 queries over 8,025 keys. Short rows lose the start (16
-      // pairs of 32 tiles at most: 190 against 184 us).
+      // into the other's products from then on; short rows lose the start. In every CTA against in
+      // none, 32 heads (16), us: prompts of 32 tiles 167 / 164 (106 / 104), 40: 248 / 246, 48:
+      // 344 / 346 (226 / 208), 64: 593 / 599 (324 / 332), 96 at 4 heads 251 / 283; 1,024 queries
+      // behind a prefix, where all CTAs are long, 32 tiles in all 92 / 99, 40: 107 / 115, 64:
+      // 155 / 170. (The rule goes by a CTA's own tiles, so a prompt's first pairs start together.)
       if (x == 1 && nt[0] >= LATE_START) alive = alive && wait(&bars[B_START], 0);
       for (int j = -1; j < n_tiles && alive; ++j) {
         if (j >= 0) {

@@ -36,6 +36,8 @@
  *   - Tensor pointers must be 16-byte aligned; tensors are dense, row-major,
  *     token-major with the strides implied by the shapes below.
  *   - Outputs may not alias inputs (except the decode state, updated in place).
+ *   - Any host thread may call, several at the same time, also one that has made no CUDA call
+ *     before; a call works on the thread's current device, to which `stream` must belong.
  */
 #ifndef KDA_B200_H
 #define KDA_B200_H
@@ -535,8 +537,8 @@ int kda_mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const
  *            set; it must stay untouched until the stream has passed the call: calls that may
  *            overlap on the GPU need one each.
  * Results do not depend on timing: the parts of a sequence are joined in a fixed order.
- * Precision: as kda_mla_prefill, where a part is a sequence's share of one CTA's run: the rows of all
- * sequences (times the groups of 64 (token, head) rows) over the SMs, at most 131,072 for 0.1 %.
+ * Precision: as kda_mla_prefill, but a part is one SM's share of all sequences' rows: 2^-23 for every
+ * 16 of them, 0.1 % at 131,072 rows of one sequence per SM (some 19 million in the call).
  * Returns KDA_OK or a negative kda_status.
  */
 size_t kda_mla_decode_workspace_size(int32_t n_tokens, int32_t n_heads);
