@@ -257,3 +257,21 @@ def test_decode_most_rows(kda, tree):
     assert torch.equal(fin, torch.isfinite(lse[:, :, part]))
     assert float((l1 - lse[:, :, part])[fin].abs().max()) <= 1e-4
     assert float((o1.float() - o[:, :, part].float()).abs().max()) <= 2 * H8 * float(o1.float().abs().max())
+
+
+@pytest.mark.parametrize("page,most", [(1 << 15, 1 << 15), (8, 1 << 20)])
+def test_widest_page_table(kda, page, most):
+    """A table for 2^30 rows a sequence (or of a million pages), of which a few are there; the rest of its
+    entries are -1 and never read."""
+    L = 1000
+    used = -(-L // page)
+    table = torch.full((2, most), -1, dtype=torch.int32, device="cuda")
+    table[0, :used] = torch.arange(used, device="cuda", dtype=torch.int32)
+    table[1, :used] = torch.arange(used, 2 * used, device="cuda", dtype=torch.int32)
+    cache = torch.full((2 * used, page, W), float("nan"), device="cuda", dtype=torch.bfloat16)
+    x = torch.randn(2 * L, W, device="cuda").bfloat16()
+    lens = i32([L, L])
+    kda.mla_append(x, None, cache, table, lens)
+    q = (torch.randn(2, 1, 4, W, device="cuda") * 0.577).bfloat16()
+    o, lse = kda.mla_decode(q, cache, table, lens, output_lse=True)
+    check_decode(o, lse, q, cache, table, lens, [0, 1])

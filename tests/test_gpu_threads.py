@@ -144,3 +144,37 @@ def test_token_runs_of_several_sizes_at_once(kda, tokens, dtype):
     assert run_at_once(lib.kda_decode_tokens, args, 10000) == []
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
     assert kda.device_status() == 0
+
+
+def test_all_kinds_on_streams_of_their_own(kda):
+    """Every kind of call, each over and over from a thread and a stream of its own: the kernels share the
+    SMs' tensor and shared memory, and none its results."""
+    torch.manual_seed(1)
+    named = calls(kda)
+    want = {}
+    for name, (call, out) in named.items():
+        call()
+        want[name] = out.clone()
+        out.zero_()
+    torch.cuda.synchronize()
+    errors, go = [], threading.Barrier(len(named))
+
+    def work(call):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                go.wait()
+                for _ in range(500):
+                    call()
+        except Exception as e:   # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(call,)) for call, _ in named.values()]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert errors == []
+    for name, (_, out) in named.items():
+        assert torch.equal(out, want[name]), name
+    assert kda.device_status() == 0
