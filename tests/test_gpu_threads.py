@@ -124,6 +124,7 @@ def test_trees_of_several_sizes_at_once(kda, tokens, dtype):
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
     assert kda.device_status() == 0
 
+
 @pytest.mark.parametrize("tokens", [(1, 2, 1, 2), (3, 8, 4, 7), (12, 16, 13, 15)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_token_runs_of_several_sizes_at_once(kda, tokens, dtype):
